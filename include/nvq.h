@@ -365,6 +365,115 @@ NVQ_API int nvfp4_linear_short_m(const void* x, int64_t M, int64_t K, int64_t ld
                                  nvq_stream_t stream);
 
 /*
+ * FP8 with one FP32 scale per block of 128.
+ *
+ * E4M3 codes (one byte, row-major, dense: pitch = columns) of a matrix, with
+ * FP32 scales of its blocks, value = code * scale.  A matrix is quantized in one
+ * of three ways, by what the product that reads it contracts:
+ *   rows     1 x 128 blocks along a row; scales [ceil(cols / 128)][rows], the
+ *            scale of (r, c) at (c / 128) * rows + r.  Activations and output
+ *            gradients of a product that contracts the columns.
+ *   columns  128 x 1 blocks along a column; scales [ceil(rows / 128)][cols], the
+ *            scale of (r, c) at (r / 128) * cols + c.  Operands of a weight
+ *            gradient, which contracts the rows (tokens).
+ *   tiles    128 x 128 blocks; scales [ceil(rows / 128)][ceil(cols / 128)].  Weights;
+ *            the same codes and scales serve the product and its input gradient.
+ * Blocks at a ragged end are short.  Products sum each block's codes on the
+ * tensor cores, apply both FP32 scales to the block's sum and add it to an FP32
+ * total, so scales may be any FP32 numbers, not only powers of two.  The
+ * product of two blocks' scales must be a normal FP32 number (or 0).
+ *
+ * Shapes: in a layer out = in . W^T with W [N, K], N is a multiple of 8 and K of
+ * 16 (a quantizer alone takes any multiple of 8 columns); row counts are any (0:
+ * an empty batch); BF16 (FP32) pitches are multiples of 8 (4) elements; pointers
+ * 16-byte aligned; every matrix less than 2^31 elements.  Otherwise NVQ_ERR_SHAPE /
+ * NVQ_ERR_ALIGN and nothing is launched.  No entry point needs a workspace; all
+ * can be captured into a CUDA graph, and calls that share no output can run at
+ * the same time.  These entry points have no counterpart on the pages, whose
+ * formats are NVFP4 and MXFP8.
+ */
+
+enum { NVQ_FP8_ROWS = 0, NVQ_FP8_COLUMNS = 1, NVQ_FP8_TILES = 2 };
+
+/* Number of FP32 scales of a [rows, cols] matrix quantized by `kind` (0 for an
+ * unknown kind or an empty matrix). */
+NVQ_API size_t fp8_block_scales(int kind, int64_t rows, int64_t cols);
+
+/*
+ * fp8_block_quantize -- BF16 [M, K] (pitch ldx) to row-wise and / or column-wise
+ * FP8 in one pass over x.  Either pair of outputs may be NULL, not both.
+ *
+ * Per block with b = max |x|, in FP32 round-to-nearest-even: scale = b / 448,
+ * r = 448 / b, code = E4M3(x * r) to nearest even.  b < 2^-100 (zero included)
+ * gives scale 0 and codes +-0.  A NaN in a block makes its scale NaN; an
+ * infinity makes the scale infinite and its own code NaN; either sets
+ * NVQ_STATUS_NONFINITE, and every product that reads the block is NaN there.
+ */
+NVQ_API int fp8_block_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* row_codes, float* row_scales,
+                               uint8_t* col_codes, float* col_scales, nvq_stream_t stream);
+
+/* fp8_block_quantize_weight -- BF16 [N, K] (pitch ldw) to tile-wise FP8, the
+ * same arithmetic with 128 x 128 blocks. */
+NVQ_API int fp8_block_quantize_weight(const void* w, int64_t N, int64_t K, int64_t ldw, uint8_t* codes, float* scales,
+                                      nvq_stream_t stream);
+
+/*
+ * fp8_block_linear -- out[M, N] = bf16( A . W^T + bias ), A [M, K] row-wise, W
+ * [N, K] tile-wise, bias NULL or BF16 [N]; N a multiple of 8.
+ */
+NVQ_API int fp8_block_linear(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
+                             const float* w_scales, const void* bias, void* out, int64_t ldo, int64_t M, int64_t N,
+                             int64_t K, nvq_stream_t stream);
+
+/*
+ * fp8_block_linear_dgrad -- the input gradient dX[M, K] = bf16( dY . W ), dY
+ * [M, N] row-wise, W [N, K] tile-wise as fp8_block_linear takes it (no
+ * transposed copy).
+ */
+NVQ_API int fp8_block_linear_dgrad(const uint8_t* dy_codes, const float* dy_scales, const uint8_t* w_codes,
+                                   const float* w_scales, void* dx, int64_t lddx, int64_t M, int64_t N, int64_t K,
+                                   nvq_stream_t stream);
+
+/*
+ * fp8_block_linear_wgrad -- the weight gradient dW[N, K] = dY^T . X in FP32, dY
+ * [M, N] and X [M, K] column-wise; accumulate != 0 adds to dW (gradient
+ * accumulation over micro-batches; one addition per element, so the result does
+ * not depend on timing).  M == 0 writes zeros (or adds nothing).
+ */
+NVQ_API int fp8_block_linear_wgrad(const uint8_t* dy_codes, const float* dy_scales, const uint8_t* x_codes,
+                                   const float* x_scales, float* dw, int64_t lddw, int accumulate, int64_t M,
+                                   int64_t N, int64_t K, nvq_stream_t stream);
+
+/*
+ * fp8_block_gated_linear -- the first half of a gated feed-forward block in one
+ * kernel: gate = A . Wg^T, up = A . Wu^T, H = SiLU(gate) * up, with
+ * SiLU(g) = g / (1 + exp(-g)), H quantized row-wise for the second projection.
+ *
+ *   a_codes, a_scales  [M, K] row-wise
+ *   w_codes, w_scales  [2F, K] tile-wise: rows 0 .. F-1 are Wg, F .. 2F-1 are Wu; F a multiple of 128
+ *   h_codes, h_scales  out, [M, F] row-wise, of the FP32 H (gate and up are not rounded on the way)
+ *   gate_up            NULL (serving), or out BF16 [M, 2F], pitch ldgu: what fp8_block_gated_backward reads
+ */
+NVQ_API int fp8_block_gated_linear(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
+                                   const float* w_scales, uint8_t* h_codes, float* h_scales, void* gate_up,
+                                   int64_t ldgu, int64_t M, int64_t F, int64_t K, nvq_stream_t stream);
+
+/*
+ * fp8_block_gated_backward -- the gradients of gate and up, and H again, as the
+ * products that follow read them, in one pass:
+ *   s = 1 / (1 + exp(-gate)), dgate = dH * up * s * (1 + gate * (1 - s)), dup = dH * gate * s
+ *
+ *   dh, gate_up          BF16 [M, F] (pitch lddh) and [M, 2F] (pitch ldgu)
+ *   row_codes, row_scales   out, [dgate | dup] [M, 2F] row-wise (for fp8_block_linear_dgrad with the [2F, K] weight)
+ *   col_codes, col_scales   out, the same column-wise (for fp8_block_linear_wgrad)
+ *   h_codes, h_scales       out, H [M, F] column-wise (the second projection's fp8_block_linear_wgrad)
+ * F a multiple of 128.
+ */
+NVQ_API int fp8_block_gated_backward(const void* dh, int64_t lddh, const void* gate_up, int64_t ldgu,
+                                     uint8_t* row_codes, float* row_scales, uint8_t* col_codes, float* col_scales,
+                                     uint8_t* h_codes, float* h_scales, int64_t M, int64_t F, nvq_stream_t stream);
+
+/*
  * nvq_device_status -- synchronizes `stream`, then returns the current
  * device's status word (NVQ_STATUS_* bits, 0 = clean) and clears it.
  * Returns NVQ_ERR_CUDA (< 0) if the synchronization or the read fails.

@@ -14,6 +14,14 @@ helpers, the status word and the test hooks.  ``QuantizedLinear`` sequences
 them for a caller: weight quantized once, then per call the activation's
 quantization and the GEMM (one launch for NVFP4 batches of at most 8 rows).
 
+FP8 with one FP32 scale per block of 128: ``fp8_block_quantize`` (row-wise),
+``fp8_block_quantize_columns``, ``fp8_block_quantize_both`` and
+``fp8_block_quantize_weight``; the products ``fp8_block_linear``,
+``fp8_block_linear_dgrad`` and ``fp8_block_linear_wgrad``; the gated
+feed-forward's ``fp8_block_gated_linear`` and ``fp8_block_gated_backward``.
+``BlockFp8Linear`` and ``BlockFp8GatedFF`` sequence them for a caller, forward
+and backward.
+
 With NVQ_DEBUG=1 in the environment at import, the debug build
 ``libnvq_debug.so`` (bounds-checked kernels, see ``build.py``) is loaded
 instead; ``DEBUG_BUILD`` says which one is in use.
@@ -104,12 +112,27 @@ _lib.nvq_gemm_plan_host.restype = ctypes.c_int
 _lib.nvq_gemm_plan_host.argtypes = [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, ctypes.c_int, ctypes.c_int,
                                     _vp, _vp, _vp]
 
+_lib.fp8_block_scales.restype = _sz
+_lib.fp8_block_scales.argtypes = [ctypes.c_int, _i64, _i64]
+for _name, _args in (
+        ("fp8_block_quantize", [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+        ("fp8_block_quantize_weight", [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+        ("fp8_block_linear", [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+        ("fp8_block_linear_dgrad", [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+        ("fp8_block_linear_wgrad", [_vp, _vp, _vp, _vp, _vp, _i64, ctypes.c_int, _i64, _i64, _i64, _vp]),
+        ("fp8_block_gated_linear", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+        ("fp8_block_gated_backward", [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp])):
+    getattr(_lib, _name).restype = ctypes.c_int
+    getattr(_lib, _name).argtypes = _args
+
 EXPORTED = ("nvq_codes_bytes", "nvq_scale_bytes", "nvq_workspace_bytes", "nvfp4_quantize",
             "mxfp8_quantize", "mxfp8_quantize_ex", "quantize_weight", "block_scaled_linear",
             "nvq_device_status", "nvq_status_string", "nvq_probe_convert", "nvfp4_quantize_noalloc",
             "block_scaled_linear_gelu_mxfp8", "nvq_probe_gelu", "nvq_probe_wait", "nvq_gemm_plan",
             "nvq_gemm_plan_host", "nvq_set_wait_limit", "nvq_workspace_init", "nvq_debug_build",
-            "nvq_probe_bounds", "nvfp4_linear_short_m", "nvq_wait_limit")
+            "nvq_probe_bounds", "nvfp4_linear_short_m", "nvq_wait_limit", "fp8_block_scales",
+            "fp8_block_quantize", "fp8_block_quantize_weight", "fp8_block_linear", "fp8_block_linear_dgrad",
+            "fp8_block_linear_wgrad", "fp8_block_gated_linear", "fp8_block_gated_backward")
 
 DEBUG_BUILD = bool(_lib.nvq_debug_build())
 
@@ -466,6 +489,291 @@ class QuantizedLinear:
             g = None
         return block_scaled_linear(self.fmt, codes, scales, g, self.w_codes, self.w_scales, self.w_global,
                                    M, self.N, self.K, bias=self.bias, out=out, stream=stream)
+
+
+# --------------------------------------------------------------------------- FP8, one scale per block of 128
+
+FP8_ROWS, FP8_COLUMNS, FP8_TILES = 0, 1, 2
+_FP8_KINDS = {"rows": FP8_ROWS, "columns": FP8_COLUMNS, "tiles": FP8_TILES}
+_e4m3 = torch.float8_e4m3fn
+
+
+def fp8_block_scale_shape(kind, rows, cols):
+    """Shape of the FP32 scales of a [rows, cols] matrix: kind "rows" (1 x 128
+    blocks), "columns" (128 x 1) or "tiles" (128 x 128)."""
+    if kind not in _FP8_KINDS:
+        raise ValueError("unknown kind %r" % (kind,))
+    rb, cb = (rows + 127) // 128, (cols + 127) // 128
+    return {"rows": (cb, rows), "columns": (rb, cols), "tiles": (rb, cb)}[kind]
+
+
+def _codes(t, name, shape=None):
+    """A dense matrix of E4M3 codes (uint8 or float8_e4m3fn), optionally of a given shape."""
+    if t.dtype != torch.uint8 and t.dtype != _e4m3:
+        raise ValueError("%s: expected uint8 or float8_e4m3fn codes, got %s" % (name, t.dtype))
+    if t.dim() != 2 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s: expected a contiguous %s, got shape %s strides %s"
+                         % (name, "matrix" if shape is None else "[%d, %d] matrix" % shape, tuple(t.shape),
+                            tuple(t.stride())))
+    return t
+
+
+def _scales(t, name, shape):
+    if t.dtype != torch.float32:
+        raise ValueError("%s: expected torch.float32, got %s" % (name, t.dtype))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous [%d, %d] matrix, got shape %s strides %s"
+                         % (name, shape[0], shape[1], tuple(t.shape), tuple(t.stride())))
+    return t
+
+
+def _bf16(t, name, rows=None, cols=None):
+    """A row-major BF16 matrix with unit column stride; a single row may have any pitch."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s: expected torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s: expected a %smatrix with unit column stride, got shape %s strides %s"
+                         % (name, "" if rows is None else "[%d, %d] " % (rows, cols), tuple(t.shape), tuple(t.stride())))
+    return t
+
+
+def _ld(t):
+    # the pitch of one row (or none) is not read: give the kernel a valid one
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+class _Call:
+    """Runs one library call on the tensors' device and the given (or current)
+    stream.  Outputs are allocated inside, so that they belong to that stream;
+    tensors used on a stream other than the current one are recorded on it, so
+    that their memory is not handed out again while the call may still run."""
+
+    def __init__(self, stream, **tensors):
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("%s: expected a CUDA tensor" % name)
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("%s: on %s, the other tensors on %s" % (name, t.device, dev))
+        self.device = dev
+        self.tensors = tensors
+        self.stream = stream
+        self.guard = None
+        if stream is not None and stream.device != dev:
+            raise ValueError("stream: on %s, the tensors on %s" % (stream.device, dev))
+
+    def __enter__(self):
+        if self.stream is not None and self.stream != torch.cuda.current_stream(self.device):
+            self.guard = torch.cuda.stream(self.stream)         # also makes its device current
+            self.guard.__enter__()
+            for t in self.tensors.values():
+                if t is not None:
+                    t.record_stream(self.stream)
+        elif self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        self.raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def fp8_block_quantize(x, codes=None, scales=None, stream=None):
+    """BF16 [M, K] -> (codes u8 [M, K], scales f32 [ceil(K / 128), M]): E4M3
+    with one scale per 1 x 128 block of a row.  K a multiple of 8 (of 16 for
+    the products)."""
+    _bf16(x, "x")
+    M, K = x.shape
+    if codes is not None:
+        _codes(codes, "codes", (M, K))
+    if scales is not None:
+        _scales(scales, "scales", ((K + 127) // 128, M))
+    with _Call(stream, x=x, codes=codes, scales=scales) as c:
+        if codes is None:
+            codes = c.empty((M, K), torch.uint8)
+        if scales is None:
+            scales = c.empty(((K + 127) // 128, M), torch.float32)
+        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), codes.data_ptr(), scales.data_ptr(), None, None,
+                                       c.raw), "fp8_block_quantize")
+    return codes, scales
+
+
+def fp8_block_quantize_columns(x, codes=None, scales=None, stream=None):
+    """BF16 [M, K] -> (codes u8 [M, K], scales f32 [ceil(M / 128), K]): E4M3
+    with one scale per 128 x 1 block of a column."""
+    _bf16(x, "x")
+    M, K = x.shape
+    if codes is not None:
+        _codes(codes, "codes", (M, K))
+    if scales is not None:
+        _scales(scales, "scales", ((M + 127) // 128, K))
+    with _Call(stream, x=x, codes=codes, scales=scales) as c:
+        if codes is None:
+            codes = c.empty((M, K), torch.uint8)
+        if scales is None:
+            scales = c.empty(((M + 127) // 128, K), torch.float32)
+        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), None, None, codes.data_ptr(), scales.data_ptr(),
+                                       c.raw), "fp8_block_quantize")
+    return codes, scales
+
+
+def fp8_block_quantize_both(x, stream=None):
+    """fp8_block_quantize and fp8_block_quantize_columns in one pass over x:
+    (row codes, row scales, column codes, column scales)."""
+    _bf16(x, "x")
+    M, K = x.shape
+    with _Call(stream, x=x) as c:
+        rc, cc = c.empty((M, K), torch.uint8), c.empty((M, K), torch.uint8)
+        rs = c.empty(((K + 127) // 128, M), torch.float32)
+        cs = c.empty(((M + 127) // 128, K), torch.float32)
+        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), rc.data_ptr(), rs.data_ptr(), cc.data_ptr(),
+                                       cs.data_ptr(), c.raw), "fp8_block_quantize")
+    return rc, rs, cc, cs
+
+
+def fp8_block_quantize_weight(w, codes=None, scales=None, stream=None):
+    """BF16 [N, K] -> (codes u8 [N, K], scales f32 [ceil(N / 128), ceil(K / 128)]):
+    E4M3 with one scale per 128 x 128 block."""
+    _bf16(w, "w")
+    N, K = w.shape
+    shape = ((N + 127) // 128, (K + 127) // 128)
+    if codes is not None:
+        _codes(codes, "codes", (N, K))
+    if scales is not None:
+        _scales(scales, "scales", shape)
+    with _Call(stream, w=w, codes=codes, scales=scales) as c:
+        if codes is None:
+            codes = c.empty((N, K), torch.uint8)
+        if scales is None:
+            scales = c.empty(shape, torch.float32)
+        _check(_lib.fp8_block_quantize_weight(w.data_ptr(), N, K, _ld(w), codes.data_ptr(), scales.data_ptr(), c.raw),
+               "fp8_block_quantize_weight")
+    return codes, scales
+
+
+def _fp8_pair(a_codes, a_scales, w_codes, w_scales, names):
+    """Row-wise codes [M, T] and a tile-wise weight; returns (M, T, weight rows, weight columns)."""
+    _codes(a_codes, names[0] + "_codes")
+    _codes(w_codes, names[1] + "_codes")
+    M, T = a_codes.shape
+    N, K = w_codes.shape
+    _scales(a_scales, names[0] + "_scales", ((T + 127) // 128, M))
+    _scales(w_scales, names[1] + "_scales", ((N + 127) // 128, (K + 127) // 128))
+    return M, T, N, K
+
+
+def fp8_block_linear(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, stream=None):
+    """out = bf16(A . W^T + bias), A [M, K] from fp8_block_quantize, W [N, K]
+    from fp8_block_quantize_weight; returns out [M, N]."""
+    M, K, N, Kw = _fp8_pair(a_codes, a_scales, w_codes, w_scales, ("a", "w"))
+    if K != Kw:
+        raise ValueError("a_codes has %d columns, w_codes %d" % (K, Kw))
+    if bias is not None:
+        _buf(bias, torch.bfloat16, 2 * N, "bias")
+    if out is not None:
+        _bf16(out, "out", M, N)
+    with _Call(stream, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out) as c:
+        if out is None:
+            out = c.empty((M, N), torch.bfloat16)
+        _check(_lib.fp8_block_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                     None if bias is None else bias.data_ptr(), out.data_ptr(), _ld(out), M, N, K,
+                                     c.raw), "fp8_block_linear")
+    return out
+
+
+def fp8_block_linear_dgrad(dy_codes, dy_scales, w_codes, w_scales, out=None, stream=None):
+    """The input gradient bf16(dY . W): dY [M, N] row-wise, W [N, K] as
+    fp8_block_linear takes it; returns dX [M, K]."""
+    M, Nd, N, K = _fp8_pair(dy_codes, dy_scales, w_codes, w_scales, ("dy", "w"))
+    if Nd != N:
+        raise ValueError("dy_codes has %d columns, w_codes %d rows" % (Nd, N))
+    if out is not None:
+        _bf16(out, "out", M, K)
+    with _Call(stream, dy_codes=dy_codes, dy_scales=dy_scales, w_codes=w_codes, w_scales=w_scales, out=out) as c:
+        if out is None:
+            out = c.empty((M, K), torch.bfloat16)
+        _check(_lib.fp8_block_linear_dgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), w_codes.data_ptr(),
+                                           w_scales.data_ptr(), out.data_ptr(), _ld(out), M, N, K, c.raw),
+               "fp8_block_linear_dgrad")
+    return out
+
+
+def fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out=None, accumulate=False, stream=None):
+    """The weight gradient dY^T . X in FP32: dY [M, N] and X [M, K] column-wise
+    (fp8_block_quantize_columns or _both); returns dW [N, K].  accumulate=True
+    adds to `out`, which must then be given."""
+    _codes(dy_codes, "dy_codes")
+    _codes(x_codes, "x_codes")
+    M, N = dy_codes.shape
+    K = x_codes.shape[1]
+    if x_codes.shape[0] != M:
+        raise ValueError("dy_codes has %d rows, x_codes %d" % (M, x_codes.shape[0]))
+    _scales(dy_scales, "dy_scales", ((M + 127) // 128, N))
+    _scales(x_scales, "x_scales", ((M + 127) // 128, K))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+    else:
+        _mat(out, torch.float32, N, K, "out")
+    with _Call(stream, dy_codes=dy_codes, dy_scales=dy_scales, x_codes=x_codes, x_scales=x_scales, out=out) as c:
+        if out is None:
+            out = c.empty((N, K), torch.float32)
+        _check(_lib.fp8_block_linear_wgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), x_codes.data_ptr(),
+                                           x_scales.data_ptr(), out.data_ptr(), _ld(out), int(bool(accumulate)), M, N,
+                                           K, c.raw), "fp8_block_linear_wgrad")
+    return out
+
+
+def fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save=False, stream=None):
+    """H = SiLU(A . Wg^T) * (A . Wu^T) in one kernel, quantized row-wise:
+    (codes u8 [M, F], scales f32 [F / 128, M], gate and up).  W [2F, K]
+    tile-wise holds Wg above Wu, F a multiple of 128.  The last is None, or with
+    save=True BF16 [M, 2F] for fp8_block_gated_backward."""
+    M, K, N, Kw = _fp8_pair(a_codes, a_scales, w_codes, w_scales, ("a", "w"))
+    if K != Kw:
+        raise ValueError("a_codes has %d columns, w_codes %d" % (K, Kw))
+    if N % 256:
+        raise ValueError("w_codes: %d rows, expected gate and up of a multiple of 128 each" % N)
+    F = N // 2
+    with _Call(stream, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales) as c:
+        codes = c.empty((M, F), torch.uint8)
+        scales = c.empty((F // 128, M), torch.float32)
+        gate_up = c.empty((M, N), torch.bfloat16) if save else None
+        _check(_lib.fp8_block_gated_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
+                                           w_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                           gate_up.data_ptr() if save else None, N, M, F, K, c.raw),
+               "fp8_block_gated_linear")
+    return codes, scales, gate_up
+
+
+def fp8_block_gated_backward(dh, gate_up, stream=None):
+    """The backward pass of SiLU(gate) * up in one pass: from dH BF16 [M, F] and
+    gate and up BF16 [M, 2F], ((codes, scales) of [dgate | dup] row-wise, the
+    same column-wise, (codes, scales) of H column-wise)."""
+    _bf16(dh, "dh")
+    M, F = dh.shape
+    _bf16(gate_up, "gate_up", M, 2 * F)
+    MB = (M + 127) // 128
+    with _Call(stream, dh=dh, gate_up=gate_up) as c:
+        rc, cc = c.empty((2, M, 2 * F), torch.uint8).unbind(0)
+        rs = c.empty(((2 * F + 127) // 128, M), torch.float32)
+        cs = c.empty((MB, 2 * F), torch.float32)
+        hc = c.empty((M, F), torch.uint8)
+        hs = c.empty((MB, F), torch.float32)
+        _check(_lib.fp8_block_gated_backward(dh.data_ptr(), _ld(dh), gate_up.data_ptr(), _ld(gate_up), rc.data_ptr(),
+                                             rs.data_ptr(), cc.data_ptr(), cs.data_ptr(), hc.data_ptr(), hs.data_ptr(),
+                                             M, F, c.raw), "fp8_block_gated_backward")
+    return (rc, rs), (cc, cs), (hc, hs)
 
 
 # --------------------------------------------------------------------------- diagnostics

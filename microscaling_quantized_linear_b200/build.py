@@ -6,14 +6,17 @@ against the extents of the buffers it was given and reports a failed check in
 the device status word (NVQ_STATUS_BOUNDS) instead of making the access.  The
 package loads it in place of ``libnvq.so`` when NVQ_DEBUG=1 is set.
 
-One translation unit (``csrc/nvq.cu``) holds the C ABI and includes the
-kernels; the CUDA runtime is linked statically and the driver API is reached
-through ``cudaGetDriverEntryPoint``, so the library loads on a machine
-without a GPU driver (it then reports errors from its entry points).
+Two translation units hold the C ABI and include the kernels, compiled side
+by side: ``csrc/nvq.cu`` (NVFP4 and MXFP8) and ``csrc/fp8_block.cu`` (FP8 with
+a scale per block of 128).  The CUDA runtime is linked statically and the
+driver API is reached through ``cudaGetDriverEntryPoint``, so the library loads
+on a machine without a GPU driver (it then reports errors from its entry
+points).
 """
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,7 +28,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "-cudart", "static",
     # scale arithmetic must stay IEEE FP32 round-to-nearest in program order
     "-fmad=false", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
@@ -34,7 +37,7 @@ NVCC_FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))]
+    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))]
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -42,11 +45,17 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     deps = sources() + [os.path.join(ROOT, "include", "nvq.h"), __file__]
     if not force and os.path.exists(lib) and all(os.path.getmtime(lib) >= os.path.getmtime(d) for d in deps):
         return lib
-    tmp = lib + ".tmp.%d" % os.getpid()
-    cmd = [NVCC, *NVCC_FLAGS, *(["-DNVQ_DEBUG"] if debug else []), *(["-Xptxas", "-v"] if verbose else []),
-           os.path.join(CSRC, "nvq.cu"), "-o", tmp]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, lib)
+    units = [f for f in sources() if f.endswith(".cu")]
+    flags = [*NVCC_FLAGS, *(["-DNVQ_DEBUG"] if debug else []), *(["-Xptxas", "-v"] if verbose else [])]
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(u) + ".o") for u in units]
+        jobs = [subprocess.Popen([NVCC, *flags, "-c", u, "-o", o]) for u, o in zip(units, objs)]
+        codes = [j.wait() for j in jobs]
+        if any(codes):
+            raise subprocess.CalledProcessError(next(c for c in codes if c), NVCC)
+        out = lib + ".tmp.%d" % os.getpid()
+        subprocess.run([NVCC, *flags, "-shared", *objs, "-o", out], check=True)
+    os.replace(out, lib)
     return lib
 
 

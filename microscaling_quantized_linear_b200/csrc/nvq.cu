@@ -16,6 +16,7 @@
 #include "nvq.h"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
+#include "host.h"
 #include "quantize.cuh"
 
 namespace nvq {
@@ -60,10 +61,7 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
+HostEncodeTiledFn g_encode = nullptr;
 
 int device_info(DeviceInfo** out) {
     int dev = 0;
@@ -98,7 +96,7 @@ int get_encoder() {
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess || fn == nullptr)
         return NVQ_ERR_CUDA;
-    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+    g_encode = reinterpret_cast<HostEncodeTiledFn>(fn);
     return NVQ_OK;
 }
 
@@ -828,6 +826,17 @@ int launch_gelu_mxfp8(DeviceInfo* d, const uint8_t* a_codes, const uint8_t* a_sc
     return launch_gemm<FMT, 256, 1>(d, a_codes, a_scales, a_global, b_codes, b_scales, b_global, bias, nullptr, 0,
                                     y_codes, y_scales, M, N, K, s);
 }
+
+int host_device(HostDevice* out) {
+    DeviceInfo* d = nullptr;
+    if (int rc = device_info(&d)) return rc;
+    *out = {static_cast<int>(d - g_dev), d->num_sms, d->status};
+    return NVQ_OK;
+}
+
+HostEncodeTiledFn host_encoder() { return get_encoder() == NVQ_OK ? g_encode : nullptr; }
+
+uint64_t host_wait_ns(uint64_t dflt) { return pipeline_wait_ns(dflt); }
 
 }  // namespace nvq
 

@@ -23,6 +23,7 @@
 // scalar ones); every result is bit-identical to the CPU oracle.
 #pragma once
 #include <cstdint>
+#include "amax.cuh"
 #include "debug.cuh"
 #include "ptx.cuh"
 
@@ -40,21 +41,6 @@ constexpr size_t kWorkspacePartialsOffset = (size_t)kMaxFusedCtas * kFusedSlotSt
 constexpr size_t kWorkspaceGenOffset = kWorkspacePartialsOffset + kMaxAmaxPartials * 4;
 constexpr size_t kWorkspaceBytes = kWorkspaceGenOffset + 128;
 constexpr int kQuantThreads = 256;
-constexpr float kAmaxFloor = 0x1p-100f;       // below this the tensor quantizes to zero
-
-// Bits of the device status word (the NVQ_STATUS_* values of nvq.h).
-constexpr unsigned int kStatusTimeout = 1u;
-constexpr unsigned int kStatusNonfinite = 2u;
-constexpr unsigned int kStatusWorkspace = 4u;
-
-// max over the two 16-bit magnitudes packed in u
-__device__ __forceinline__ uint32_t absmax2(uint32_t acc, uint32_t u) {
-    return __vmaxu2(acc, u & 0x7FFF7FFFu);
-}
-
-__device__ __forceinline__ uint32_t fold2(uint32_t m2) {
-    return max(m2 & 0xFFFFu, m2 >> 16);
-}
 
 // BF16 magnitude bits of the largest |x| among the 16 values in w[0..7].
 __device__ __forceinline__ uint32_t block16_max(const uint32_t (&w)[8]) {
@@ -62,19 +48,6 @@ __device__ __forceinline__ uint32_t block16_max(const uint32_t (&w)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m2 = absmax2(m2, w[i]);
     return fold2(m2);
-}
-
-// Block-wide max of one value per thread; result valid in every thread.
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_max_u32(uint32_t v, uint32_t* red /* THREADS/32 */) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    uint32_t w = (lane < THREADS / 32) ? red[lane] : 0u;
-    w = __reduce_max_sync(0xFFFFFFFFu, w);
-    __syncthreads();
-    return w;
 }
 
 // Offset of scale (row r, column c) in the 128x4 tile order, C/4 = ctiles.
