@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "fp8_gated.cuh"
@@ -56,11 +57,83 @@ int launch(void (*kernel)(KArgs...), uint32_t grid, uint32_t block, size_t smem,
     return NVQ_OK;
 }
 
-template <int OP>
-int launch_gemm(const HostDevice& d, Fp8GemmParams& p, nvq_stream_t stream) {
+// A dense [rows, cols] code matrix in tiles of 128 rows x 128 bytes, swizzled as
+// the MMA reads them; what lies outside reads as zeros.
+int codes_map(HostEncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t cols) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols};
+    const cuuint32_t box[2] = {128u, 128u}, estr[2] = {1u, 1u};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? NVQ_OK : NVQ_ERR_CUDA;
+}
+
+// The output in chunks of 32 rows x 64 bytes; stores outside are dropped.
+int out_map(HostEncodeTiledFn encode, CUtensorMap* map, void* out, bool f32, int64_t rows, int64_t cols, int64_t ld) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 16u : 32u, 32u}, estr[2] = {1u, 1u};
+    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? NVQ_OK : NVQ_ERR_CUDA;
+}
+
+struct Fp8Gemm {
+    const uint8_t *a, *b;
+    void* out;
+    int64_t ldo;
+    Fp8GemmParams p;
+};
+
+Fp8GemmParams gemm_params(const float* sa, const float* sb, int64_t R, int64_t C, int64_t T) {
+    Fp8GemmParams p = {};
+    p.sa = sa;
+    p.sb = sb;
+    p.R = (uint32_t)R;
+    p.C = (uint32_t)C;
+    p.T = (uint32_t)T;
+    return p;
+}
+
+template <int OP, bool PLAIN_A>
+int launch_pair(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
+    using C = Fp8PairCfg<OP, PLAIN_A>;
+    const HostEncodeTiledFn encode = host_encoder();
+    if (!encode) return NVQ_ERR_CUDA;
+    Fp8GemmParams& p = g.p;
+    const int64_t brows = OP == kFp8Gated ? 2 * (int64_t)p.C : p.C;
+    CUtensorMap ma, mb, mo;
+    int rc;
+    if ((rc = codes_map(encode, &mb, g.b, C::B_MN ? p.T : brows, C::B_MN ? brows : p.T))) return rc;
+    if (PLAIN_A) ma = mb;                                // not read
+    else if ((rc = codes_map(encode, &ma, g.a, C::A_MN ? p.T : p.R, C::A_MN ? p.R : p.T))) return rc;
+    if (!g.out) mo = mb;                                 // not written
+    else if ((rc = out_map(encode, &mo, g.out, OP == kFp8Wgrad, p.R, brows, g.ldo))) return rc;
+    auto kern = fp8_gemm_pair_kernel<OP, PLAIN_A>;
+    static std::atomic<uint64_t> opted{0};               // devices whose shared-memory limit is raised
+    if (!(opted.load(std::memory_order_acquire) >> d.index & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess) {
+            cudaGetLastError();
+            return NVQ_ERR_CUDA;
+        }
+        opted.fetch_or(uint64_t(1) << d.index, std::memory_order_release);
+    }
+    p.a = g.a;
     p.status = d.status;
-    const uint64_t tiles = (uint64_t)blocks_of(p.C) * ((p.R + 31) / 32);
-    return launch(fp8_gemm_simple_kernel<OP>, (uint32_t)tiles, 256, 0, stream, 1, p);
+    p.wait_ns = (uint32_t)host_wait_ns(kFp8WaitNs);
+    p.row_tiles = (p.R + 255) / 256;
+    p.col_tiles = OP == kFp8Gated ? p.C / 128 : (p.C + 255) / 256;
+    p.save = OP == kFp8Gated && g.out != nullptr;
+    const uint32_t tiles = p.row_tiles * p.col_tiles, pairs = (uint32_t)d.num_sms / 2;
+    return launch(kern, 2 * (tiles < pairs ? tiles : pairs), C::THREADS, C::SMEM_BYTES, stream, 2, ma, mb, mo, p);
+}
+
+template <int OP>
+int launch_gemm(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
+    // dY's rows may be 8 bytes past a multiple of 16, which a tensor map cannot describe
+    if constexpr (OP == kFp8Dgrad || OP == kFp8Wgrad)
+        if ((OP == kFp8Wgrad ? g.p.R : g.p.T) % 16) return launch_pair<OP, true>(d, g, stream);
+    return launch_pair<OP, false>(d, g, stream);
 }
 
 }  // namespace
@@ -122,9 +195,9 @@ int fp8_block_linear(const uint8_t* a_codes, const float* a_scales, const uint8_
         return NVQ_ERR_ALIGN;
     HostDevice d;
     if (int rc = host_device(&d)) return rc;
-    Fp8GemmParams p = {a_codes, a_scales, w_codes, w_scales, static_cast<const __nv_bfloat16*>(bias), out, nullptr,
-                       nullptr, (uint32_t)M, (uint32_t)N, (uint32_t)K, (uint32_t)ldo, 0, nullptr};
-    return launch_gemm<kFp8Linear>(d, p, stream);
+    Fp8Gemm g = {a_codes, w_codes, out, ldo, gemm_params(a_scales, w_scales, M, N, K)};
+    g.p.bias = static_cast<const __nv_bfloat16*>(bias);
+    return launch_gemm<kFp8Linear>(d, g, stream);
 }
 
 int fp8_block_linear_dgrad(const uint8_t* dy_codes, const float* dy_scales, const uint8_t* w_codes,
@@ -137,9 +210,8 @@ int fp8_block_linear_dgrad(const uint8_t* dy_codes, const float* dy_scales, cons
         return NVQ_ERR_ALIGN;
     HostDevice d;
     if (int rc = host_device(&d)) return rc;
-    Fp8GemmParams p = {dy_codes, dy_scales, w_codes, w_scales, nullptr, dx, nullptr, nullptr, (uint32_t)M, (uint32_t)K,
-                       (uint32_t)N, (uint32_t)lddx, 0, nullptr};
-    return launch_gemm<kFp8Dgrad>(d, p, stream);
+    Fp8Gemm g = {dy_codes, w_codes, dx, lddx, gemm_params(dy_scales, w_scales, M, K, N)};
+    return launch_gemm<kFp8Dgrad>(d, g, stream);
 }
 
 int fp8_block_linear_wgrad(const uint8_t* dy_codes, const float* dy_scales, const uint8_t* x_codes,
@@ -158,9 +230,9 @@ int fp8_block_linear_wgrad(const uint8_t* dy_codes, const float* dy_scales, cons
         }
         return NVQ_OK;
     }
-    Fp8GemmParams p = {dy_codes, dy_scales, x_codes, x_scales, nullptr, dw, nullptr, nullptr, (uint32_t)N, (uint32_t)K,
-                       (uint32_t)M, (uint32_t)lddw, accumulate != 0, nullptr};
-    return launch_gemm<kFp8Wgrad>(d, p, stream);
+    Fp8Gemm g = {dy_codes, x_codes, dw, lddw, gemm_params(dy_scales, x_scales, N, K, M)};
+    g.p.accumulate = accumulate != 0;
+    return launch_gemm<kFp8Wgrad>(d, g, stream);
 }
 
 int fp8_block_gated_linear(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
@@ -175,9 +247,10 @@ int fp8_block_gated_linear(const uint8_t* a_codes, const float* a_scales, const 
         return NVQ_ERR_ALIGN;
     HostDevice d;
     if (int rc = host_device(&d)) return rc;
-    Fp8GemmParams p = {a_codes, a_scales, w_codes, w_scales, nullptr, gate_up, h_codes, h_scales, (uint32_t)M,
-                       (uint32_t)F, (uint32_t)K, (uint32_t)ldgu, 0, nullptr};
-    return launch_gemm<kFp8Gated>(d, p, stream);
+    Fp8Gemm g = {a_codes, w_codes, gate_up, ldgu, gemm_params(a_scales, w_scales, M, F, K)};
+    g.p.h_codes = h_codes;
+    g.p.h_scales = h_scales;
+    return launch_gemm<kFp8Gated>(d, g, stream);
 }
 
 int fp8_block_gated_backward(const void* dh, int64_t lddh, const void* gate_up, int64_t ldgu, uint8_t* row_codes,

@@ -7,12 +7,27 @@
 // dgrad     a = dY [M, N] row-wise, b = the same weights read along N
 // wgrad     a = dY [M, N], b = X [M, K], both column-wise and read along M
 // gated     linear onto gate and up; H = SiLU(gate) * up quantized row-wise
-// The inner sum of a block is a sum of products of codes; the scales are FP32,
-// so they are applied to each block's sum as it is added to the FP32 total.
+//
+// The scales are FP32, so the tensor core cannot apply them (its own block
+// scales are powers of two): each block's sum is taken by four MMAs into tensor
+// memory, and 16 epilogue warps read it, multiply by the scales and add it to
+// the FP32 total in their registers, while the MMAs of the next block fill the
+// other half of tensor memory (2 x 256 columns).
+//
+// CTA pairs, one per two SMs, persistent over 256 x 256 output tiles (gated: 256
+// rows x 128 columns of H, gate's 128 columns and up's as one 256-wide B tile).
+// CTA r stages rows [128 r, 128 r + 128) of the A tile and of the B tile (128
+// bytes of the contracted axis, one block, per stage), holds output rows
+// [128 r, 128 r + 128) and drains them.  Operands whose contracted axis is not
+// the contiguous one (wgrad's, dgrad's weight) are staged as they lie in memory,
+// 128 of the contracted axis x 128 contiguous bytes, and read "MN-major" by the
+// MMA: no transposed copies.
+// Warps 0-15: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 and
+// 64 columns; 16: tile loads; 17: MMAs (in the leader CTA) and tensor memory.
+// Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include "debug.cuh"
 #include "fp8_gated.cuh"
 #include "ptx.cuh"
@@ -21,129 +36,464 @@ namespace nvq {
 
 enum Fp8Op { kFp8Linear = 0, kFp8Dgrad = 1, kFp8Wgrad = 2, kFp8Gated = 3 };
 
+constexpr uint32_t kFp8WaitNs = 4000000000u;            // 4 s per pipeline wait
+
 struct Fp8GemmParams {
-    const uint8_t* a;
-    const float* sa;
-    const uint8_t* b;
-    const float* sb;
+    const uint8_t* a;           // plain A loads only
+    const float* sa;            // [T / 128][R]
+    const float* sb;            // linear, gated: [B rows / 128][T / 128]; dgrad: [T / 128][C / 128]; wgrad: [T / 128][C]
     const __nv_bfloat16* bias;
-    void* out;                  // BF16 (linear, dgrad), FP32 (wgrad), BF16 gate and up or null (gated)
-    uint8_t* h_codes;           // gated: [R, C] and [C / 128, R]
+    uint8_t* h_codes;           // gated: [R, C] and [C / 128][R]
     float* h_scales;
-    uint32_t R, C, T;           // output rows, columns (gated: F), contracted length
-    uint32_t ldo;
-    uint32_t accumulate;        // wgrad: add to out
     unsigned int* status;
+    uint32_t R, C, T;           // output rows, columns (gated: F), contracted length
+    uint32_t row_tiles, col_tiles;
+    uint32_t accumulate;        // wgrad: add to out
+    uint32_t save;              // gated: store gate and up
+    uint32_t wait_ns;
 };
 
-__device__ __forceinline__ float e4m3_value(uint8_t code) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
-}
+template <int OP, bool PLAIN_A = false>
+struct Fp8PairCfg {
+    static constexpr bool A_MN = OP == kFp8Wgrad;                       // A's contiguous axis is its row axis
+    static constexpr bool B_MN = OP == kFp8Wgrad || OP == kFp8Dgrad;
+    static constexpr bool SB_COL = OP == kFp8Wgrad;                     // one B scale per column
+    static constexpr int EPI_WARPS = 16;
+    static constexpr int LOAD_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
+    static constexpr int THREADS = 32 * (EPI_WARPS + 2);
+    static constexpr int TILE_BYTES = 128 * 128;                        // 128 rows x 128 bytes
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;                  // A and B tile of one CTA
+    static constexpr int STAGING = 32 * 64;                             // per epilogue warp
+    static constexpr int SB_BYTES = SB_COL ? EPI_WARPS * 2 * 256 : 0;   // per warp, two blocks of 64 scales
+    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 2 * 128 * 16 : 0;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int SMEM_LIMIT = 232448;
+    static constexpr int FIXED = 1024 + BAR_BYTES + EPI_WARPS * STAGING + SB_BYTES + AMAX_BYTES;
+    static constexpr int FIT = (SMEM_LIMIT - FIXED) / STAGE_BYTES;
+    static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+    static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
+    static constexpr int OFF_SB = OFF_STAGING + EPI_WARPS * STAGING;
+    static constexpr int OFF_AMAX = OFF_SB + SB_BYTES;
+    static constexpr int OFF_BAR = OFF_AMAX + AMAX_BYTES;
+    static constexpr int SMEM_BYTES = OFF_BAR + BAR_BYTES + 1024;
+    // instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 x E4M3, major-ness, N / 8, M / 16
+    static constexpr uint32_t IDESC = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+                                      ((256u >> 3) << 17) | ((256u >> 4) << 24);
+    // K step of 32 within a stage: 32 bytes along a row, or 32 rows of 128 bytes
+    static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
+    static_assert(STAGES >= 4 && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+    static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barriers");
+};
 
-template <int OP>
-__device__ __forceinline__ float fp8_a(const Fp8GemmParams& p, uint32_t r, uint32_t t) {
-    if (r >= p.R || t >= p.T) return 0.0f;
-    return e4m3_value(OP == kFp8Wgrad ? p.a[(size_t)t * p.R + r] : p.a[(size_t)r * p.T + t]);
-}
-
-template <int OP>
-__device__ __forceinline__ float fp8_b(const Fp8GemmParams& p, uint32_t c, uint32_t rows, uint32_t t) {
-    if (c >= rows || t >= p.T) return 0.0f;
-    return e4m3_value(OP == kFp8Wgrad || OP == kFp8Dgrad ? p.b[(size_t)t * rows + c] : p.b[(size_t)c * p.T + t]);
-}
-
-template <int OP>
-__device__ __forceinline__ float fp8_sb(const Fp8GemmParams& p, uint32_t c, uint32_t rows, uint32_t tb) {
-    if (c >= rows) return 0.0f;
-    if (OP == kFp8Wgrad) return p.sb[(size_t)tb * rows + c];
-    if (OP == kFp8Dgrad) return p.sb[(size_t)tb * ((rows + 127) / 128) + c / 128];
-    return p.sb[(size_t)(c / 128) * ((p.T + 127) / 128) + tb];
-}
-
-// 32 x 128 output tile (gated: of both projections), 256 threads, thread = rows
-// 4w..4w+3 of the tile (warp w) x columns 4l..4l+3 (lane l), blocks of 16 staged
-// in shared memory as FP32.
-template <int OP>
-__global__ void __launch_bounds__(256) fp8_gemm_simple_kernel(const Fp8GemmParams p) {
-    constexpr int P = OP == kFp8Gated ? 2 : 1;
-    __shared__ float s_a[16][32];
-    __shared__ float s_b[P][16][128];
-    griddep_wait();
-    griddep_launch();
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t cblocks = (p.C + 127) / 128;
-    const uint32_t c0 = (blockIdx.x % cblocks) * 128, r0 = (blockIdx.x / cblocks) * 32;
-    const uint32_t brows = P * p.C;
-    float acc[P][4][4] = {};
-    for (uint32_t tb = 0; tb * 128 < p.T; ++tb) {
-        float part[P][4][4] = {};
-        for (uint32_t k0 = tb * 128; k0 < tb * 128 + 128; k0 += 16) {
-            __syncthreads();
-            for (uint32_t i = threadIdx.x; i < 512; i += 256) s_a[i & 15][i >> 4] = fp8_a<OP>(p, r0 + (i >> 4), k0 + (i & 15));
-            for (int q = 0; q < P; ++q)
-                for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
-                    const uint32_t k = OP == kFp8Linear || OP == kFp8Gated ? i & 15 : i >> 7;
-                    const uint32_t c = OP == kFp8Linear || OP == kFp8Gated ? i >> 4 : i & 127;
-                    s_b[q][k][c] = c0 + c < p.C ? fp8_b<OP>(p, q * p.C + c0 + c, brows, k0 + k) : 0.0f;
-                }
-            __syncthreads();
-            for (int k = 0; k < 16; ++k)
-                for (int q = 0; q < P; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            part[q][i][j] = __fmaf_rn(s_a[k][warp * 4 + i], s_b[q][k][lane * 4 + j], part[q][i][j]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r = r0 + warp * 4 + i;
-            const float sa = r < p.R ? p.sa[(size_t)tb * p.R + r] : 0.0f;
-#pragma unroll
-            for (int q = 0; q < P; ++q)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t c = c0 + lane * 4 + j;
-                    const float sb = c < p.C ? fp8_sb<OP>(p, q * p.C + c, brows, tb) : 0.0f;
-                    if (r < p.R && c < p.C) acc[q][i][j] = __fmaf_rn(part[q][i][j], sa * sb, acc[q][i][j]);
-                }
+// Bounded wait of the pipeline: gives up after limit_ns or when *abort is set.
+// The clock is read on every 64th attempt only (each attempt suspends the
+// thread for a while), so a wait that is about to end costs no timer reads.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 0;; ++n) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        else
+            ok = mbar_try_wait(bar, parity);
+        if (ok) return true;
+        if ((n & 63) == 63) {
+            if (*abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > limit_ns) return false;
         }
     }
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = r0 + warp * 4 + i;
-        if (r >= p.R) continue;
-        if (OP == kFp8Gated) {
-            float hv[4];
-            uint32_t m = 0;
-            for (int j = 0; j < 4; ++j) {
-                const float gate = acc[0][i][j], up = acc[P - 1][i][j];
-                hv[j] = gate * sigmoid_f32(gate) * up;
-                m = max(m, abs_bits(hv[j]));
-                if (p.out) {
-                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)r * p.ldo + c0 + lane * 4 + j;
-                    o[0] = __float2bfloat16_rn(gate);
-                    o[p.C] = __float2bfloat16_rn(up);
+}
+
+// Stage one 128-row x 128-byte tile of a matrix whose pitch is not a multiple of
+// 16 bytes (a tensor map cannot describe it): 8-byte copies by the load warp, laid
+// out in the 128-byte swizzle that a tensor-map load would write (16-byte chunk c
+// of row r at chunk c ^ (r % 8)), zeros outside the matrix.
+__device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src, uint32_t rows, uint32_t cols, uint32_t r0,
+                                               uint32_t c0, uint32_t lane, unsigned int* status) {
+    const uint32_t c = c0 + (lane & 15) * 8;
+    const uint32_t chunk = (lane & 15) >> 1, half = (lane & 1) * 8;
+#pragma unroll 8
+    for (uint32_t i = lane >> 4; i < 128; i += 2) {
+        const uint32_t r = r0 + i;
+        const uint64_t at = (uint64_t)r * cols + c;
+        const bool in = r < rows && c < cols && in_bounds(at, 8, (uint64_t)rows * cols, status);
+        cp_async8_zfill(dst + i * 128 + ((chunk ^ (i & 7)) << 4) + half, in ? src + at : src, in ? 8 : 0);
+    }
+}
+
+// Writes one 32-row x 64-byte chunk (v: this thread's row) through the warp's
+// staging buffer: 64-byte swizzle, then a tensor-map store, or an addition.
+__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[16], uint8_t* staging, const CUtensorMap* map, int32_t c,
+                                                int32_t r, uint32_t lane, bool add) {
+    const uint32_t swz = (lane >> 1) & 3;
+    if (lane == 0) bulk_wait_group_read<0>();            // the previous store has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(staging + lane * 64 + 16 * ((uint32_t)i ^ swz)) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (add) tma_reduce_add_2d(map, smem_u32(staging), c, r);
+        else tma_store_2d(map, smem_u32(staging), c, r);
+        bulk_commit_group();
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 o = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&o);
+}
+
+template <int OP, bool PLAIN_A>
+__global__ void __launch_bounds__(Fp8PairCfg<OP, PLAIN_A>::THREADS, 1)
+fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const __grid_constant__ CUtensorMap tmap_out, const Fp8GemmParams p) {
+    using C = Fp8PairCfg<OP, PLAIN_A>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    // full[s]:   the stage's tiles of both CTAs landed (leader's barrier)
+    // empty[s]:  the stage's MMAs completed (commit multicast to both CTAs)
+    // tfull[b]:  accumulator half b holds a block's sums (both CTAs)
+    // tempty[b]: both CTAs' epilogue warps have read half b (leader's barrier)
+    const uint32_t full0 = smem_u32(bars);
+    const uint32_t empty0 = full0 + 8 * C::STAGES;
+    const uint32_t tfull0 = empty0 + 8 * C::STAGES;
+    const uint32_t tempty0 = tfull0 + 16;
+    const uint32_t drain = tempty0 + 16;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    volatile int* never = abort_flag + 1;
+
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();             // 0 = leader
+    const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full0 + 8 * s, PLAIN_A ? 3 : 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, 2 * C::EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *never = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == C::LOAD_WARP && lane == 0) {
+        if (!PLAIN_A) prefetch_tensormap(&tmap_a);
+        prefetch_tensormap(&tmap_b);
+        prefetch_tensormap(&tmap_out);
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();                                      // barriers of both CTAs initialised
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    griddep_wait();
+    griddep_launch();
+    const uint32_t num_tiles = p.row_tiles * p.col_tiles;
+    const uint32_t blocks = (p.T + 127) / 128;
+    const auto gave_up = [&] {
+        *abort_flag = 1;
+        atomicOr(p.status, kStatusTimeout);
+    };
+
+    if (warp == C::LOAD_WARP) {
+        // ---------------------------------------------------------- tile loads (both CTAs)
+        if (PLAIN_A || lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            // the plain copies of iteration j are complete: publish them to the leader's MMAs
+            const auto publish = [&](uint32_t j) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
+            };
+            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
+                const uint32_t cb = tile / p.row_tiles;
+                const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
+                for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+                    const int32_t k0 = (int32_t)(t * 128);
+                    if (lane == 0) {
+                        const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
+                        if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
+                        tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
+                    }
+                    if (PLAIN_A) {
+                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
+                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
+                        cp_async_commit();
+                        if (it > 0) {
+                            cp_async_wait<1>();
+                            publish(it - 1);
+                        }
+                    }
                 }
             }
-            m = __reduce_max_sync(0xFFFFFFFFu, m);
-            const Fp8Scale s = fp8_block_scale(m, p.status);
-            *reinterpret_cast<uint32_t*>(p.h_codes + (size_t)r * p.C + c0 + lane * 4) =
-                cvt_e4m3x4(hv[0] * s.factor, hv[1] * s.factor, hv[2] * s.factor, hv[3] * s.factor);
-            if (lane == 0) p.h_scales[(size_t)(c0 / 128) * p.R + r] = s.scale;
-            continue;
-        }
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t c = c0 + lane * 4 + j;
-            if (c >= p.C) continue;
-            float v = acc[0][i][j];
-            if (p.bias) v = __fadd_rn(v, __bfloat162float(p.bias[c]));
-            if (OP == kFp8Wgrad) {
-                float* o = static_cast<float*>(p.out) + (size_t)r * p.ldo + c;
-                *o = p.accumulate ? __fadd_rn(*o, v) : v;
-            } else {
-                static_cast<__nv_bfloat16*>(p.out)[(size_t)r * p.ldo + c] = __float2bfloat16_rn(v);
+            if (PLAIN_A && it > 0) {
+                cp_async_wait<0>();
+                publish(it - 1);
+            }
+            if (lane == 0) {
+                if (!ok) gave_up();
+                // Neither CTA leaves while a load it issued may be in flight: the leader's
+                // barriers count both CTAs' bytes; the peer learns of its own through the
+                // commits of the MMAs that consumed them.
+                for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                    fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never, kFp8WaitNs);
             }
         }
+    } else if (warp == C::MMA_WARP) {
+        // ---------------------------------------------------------- MMAs (leader)
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                    const uint32_t s = it % C::STAGES, b = it & 1, use = it >> 1;
+                    if ((use > 0 && !fp8_wait(tempty0 + 8 * b, (use - 1) & 1, abort_flag, p.wait_ns)) ||
+                        !fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        tc_mma_f8_pair(tmem + b * 256, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
+                                       smem_desc(st + C::TILE_BYTES + k * C::B_STEP, 1024, 1024, 2), C::IDESC, k != 0);
+                    tc_commit_pair_mc(empty0 + 8 * s, 0x3);
+                    tc_commit_pair_mc(tfull0 + 8 * b, 0x3);
+                }
+            }
+            if (!ok) gave_up();
+            tc_commit_pair(drain);
+            fp8_wait(drain, 0, never, kFp8WaitNs);
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue (both CTAs)
+        const uint32_t q = warp & 3, g = warp >> 2;
+        uint8_t* staging = smem + C::OFF_STAGING + warp * C::STAGING;
+        float* s_sb = reinterpret_cast<float*>(smem + C::OFF_SB + warp * 512);
+        float* s_amax = reinterpret_cast<float*>(smem + C::OFF_AMAX);
+        // this warp's two chunks of 32 columns of the 256 (gated: of gate and of up)
+        const uint32_t col0 = OP == kFp8Gated ? 32 * g : 64 * g;
+        const uint32_t col1 = OP == kFp8Gated ? 128 + 32 * g : 64 * g + 32;
+        const uint32_t lanes = tmem + ((32 * q) << 16);
+        uint32_t it = 0, tiles_done = 0;
+        bool ok = true;
+        for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs, ++tiles_done) {
+            const uint32_t rw = (tile % p.row_tiles) * 256 + 128 * rank + 32 * q;      // the warp's first row
+            const uint32_t cb = tile / p.row_tiles;
+            const uint32_t r = rw + lane, rc = min(r, p.R - 1);
+            const uint32_t n0 = cb * (OP == kFp8Gated ? 128 : 256);                    // the tile's first column
+            const uint32_t cblocks = (p.C + 127) / 128;
+            // scales of block t: the row's, and the columns' (one per 128, or one per column)
+            const float* sap = p.sa + rc;
+            const float* sbp0;
+            const float* sbp1;
+            uint32_t sb_step = 1;
+            if (OP == kFp8Gated) {
+                sbp0 = p.sb + (size_t)cb * blocks;
+                sbp1 = p.sb + (size_t)(cb + cblocks) * blocks;
+            } else {
+                const uint32_t nb = min((n0 + col0) / 128, cblocks - 1);
+                sbp0 = sbp1 = OP == kFp8Dgrad ? p.sb + nb : p.sb + (size_t)nb * blocks;
+                if (OP == kFp8Dgrad) sb_step = cblocks;
+            }
+            const uint64_t sa_n = (uint64_t)blocks * p.R, sbc_n = (uint64_t)blocks * p.C;
+            const auto row_scale = [&](uint32_t t) {
+                return t < blocks && in_bounds((uint64_t)t * p.R + rc, 1, sa_n, p.status) ? __ldg(sap + (size_t)t * p.R) : 0.0f;
+            };
+            // wgrad: this lane's two of the warp's 64 column scales (C is even)
+            const uint32_t sc = n0 + col0 + 2 * lane;
+            const auto col_scales = [&](uint32_t t) {
+                if (t < blocks && sc < p.C && in_bounds((uint64_t)t * p.C + sc, 2, sbc_n, p.status))
+                    return __ldg(reinterpret_cast<const float2*>(p.sb + (size_t)t * p.C + sc));
+                return make_float2(0.0f, 0.0f);
+            };
+            uint64_t acc0[16] = {}, acc1[16] = {};
+            float sa_a = row_scale(0), sa_b = row_scale(1);
+            float b0_a = 0, b0_b = 0, b1_a = 0, b1_b = 0;
+            float2 bc_a, bc_b;
+            if (C::SB_COL) {
+                bc_a = col_scales(0);
+                bc_b = col_scales(1);
+            } else {
+                b0_a = __ldg(sbp0);
+                b0_b = blocks > 1 ? __ldg(sbp0 + sb_step) : 0.0f;
+                if (OP == kFp8Gated) {
+                    b1_a = __ldg(sbp1);
+                    b1_b = blocks > 1 ? __ldg(sbp1 + sb_step) : 0.0f;
+                }
+            }
+            for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                const uint32_t b = it & 1;
+                const float sa = sa_a, b0 = b0_a, b1 = b1_a;
+                sa_a = sa_b;
+                sa_b = row_scale(t + 2);
+                if (C::SB_COL) {
+                    *reinterpret_cast<float2*>(s_sb + 64 * b + 2 * lane) = bc_a;
+                    bc_a = bc_b;
+                    bc_b = col_scales(t + 2);
+                    __syncwarp();
+                } else {
+                    b0_a = b0_b;
+                    b0_b = t + 2 < blocks ? __ldg(sbp0 + (size_t)(t + 2) * sb_step) : 0.0f;
+                    if (OP == kFp8Gated) {
+                        b1_a = b1_b;
+                        b1_b = t + 2 < blocks ? __ldg(sbp1 + (size_t)(t + 2) * sb_step) : 0.0f;
+                    }
+                }
+                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, b0);
+                const float f1 = OP == kFp8Gated ? __fmul_rn(sa, b1) : f0;
+                const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
+                if (!fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const auto add = [&](const uint32_t (&v)[32], uint64_t (&acc)[16], uint64_t s, const float* sb) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint64_t x = f32x2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        if (C::SB_COL) x = f32x2_mul(x, *reinterpret_cast<const uint64_t*>(sb + 2 * i));
+                        f32x2_fma(acc[i], x, s);
+                    }
+                };
+                uint32_t v[32];
+                tc_ld_32x32b_x32(lanes + b * 256 + col0, v);
+                tc_wait_ld();
+                add(v, acc0, s0, s_sb + 64 * b);
+                tc_ld_32x32b_x32(lanes + b * 256 + col1, v);
+                tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                // the loads have returned, and the signal publishes no memory writes
+                if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(tempty0 + 8 * b, 0));
+                add(v, acc1, s1, s_sb + 64 * b + 32);
+            }
+            if (!ok) break;
+            if (OP == kFp8Gated) {
+                const uint64_t h_n = (uint64_t)p.R * p.C;
+                if (p.save && rw < p.R) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = f32x2_unpack(acc0[i]);
+                        o[i] = bf16x2_of(x.x, x.y);
+                    }
+                    fp8_store_chunk(o, staging, &tmap_out, (int32_t)(n0 + col0), (int32_t)rw, lane, false);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = f32x2_unpack(acc1[i]);
+                        o[i] = bf16x2_of(x.x, x.y);
+                    }
+                    fp8_store_chunk(o, staging, &tmap_out, (int32_t)(p.C + n0 + col0), (int32_t)rw, lane, false);
+                }
+                float h[32];
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 x = f32x2_unpack(acc0[i]), u = f32x2_unpack(acc1[i]);
+                    h[2 * i] = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
+                    h[2 * i + 1] = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
+                    m = max(m, max(abs_bits(h[2 * i]), abs_bits(h[2 * i + 1])));
+                }
+                // the block of 128 columns is shared by the four warps of this lane quarter
+                uint32_t* am = reinterpret_cast<uint32_t*>(s_amax) + (tiles_done & 1) * 512 + (32 * q + lane) * 4;
+                am[g] = m;
+                named_barrier_sync(1 + q, 128);
+                const uint4 m4 = *reinterpret_cast<const uint4*>(am);
+                m = max(max(m4.x, m4.y), max(m4.z, m4.w));
+                if (r < p.R) {
+                    const Fp8Scale s = fp8_block_scale(m, p.status);
+                    const uint64_t at = (uint64_t)r * p.C + n0 + col0;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = cvt_e4m3x4(h[4 * i] * s.factor, h[4 * i + 1] * s.factor, h[4 * i + 2] * s.factor,
+                                          h[4 * i + 3] * s.factor);
+                    if (in_bounds(at, 32, h_n, p.status)) {
+                        uint4* d = reinterpret_cast<uint4*>(p.h_codes + at);
+                        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                    if (g == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
+                        p.h_scales[(size_t)cb * p.R + r] = s.scale;
+                }
+            } else if (rw < p.R) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t c = n0 + (half ? col1 : col0);
+                    const uint64_t(&acc)[16] = half ? acc1 : acc0;
+                    if (c >= p.C) continue;
+                    if (OP == kFp8Wgrad) {
+                        // 16 FP32 columns a chunk
+                        uint32_t o[16];
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 x = f32x2_unpack(acc[8 * part + i]);
+                                o[2 * i] = __float_as_uint(x.x);
+                                o[2 * i + 1] = __float_as_uint(x.y);
+                            }
+                            if (c + 16 * part < p.C)
+                                fp8_store_chunk(o, staging, &tmap_out, (int32_t)(c + 16 * part), (int32_t)rw, lane, p.accumulate);
+                        }
+                    } else {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = f32x2_unpack(acc[i]);
+                            // C is a multiple of 8, so a pair of columns is inside or outside
+                            if (OP == kFp8Linear && p.bias && c + 2 * i < p.C) {
+                                const __nv_bfloat162 bb = *reinterpret_cast<const __nv_bfloat162*>(p.bias + c + 2 * i);
+                                x.x = __fadd_rn(x.x, __bfloat162float(bb.x));
+                                x.y = __fadd_rn(x.y, __bfloat162float(bb.y));
+                            }
+                            o[i] = bf16x2_of(x.x, x.y);
+                        }
+                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)c, (int32_t)rw, lane, false);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) gave_up();
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    cluster_sync();                                      // both CTAs done with the pair's resources
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 

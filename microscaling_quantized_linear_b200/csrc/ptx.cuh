@@ -101,6 +101,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
         :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
 
+// Same, added to the destination (FP32 tensors: one FP32 addition per element).
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
+        :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1) : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -119,6 +126,11 @@ __device__ __forceinline__ void bulk_wait_group_all() {
 // 16-byte asynchronous copy global -> shared by this thread (cached in L2 only).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+
+// 8-byte asynchronous copy; `bytes` 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit() {
@@ -441,6 +453,26 @@ __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
+// D(tmem) (+)= A(smem) * B(smem), E4M3 x E4M3 without block scales, K = 32 per
+// instruction, on one CTA and on a CTA pair.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
 // ---------------------------------------------------------------- conversions
 // Two FP32 -> two E2M1 codes in one byte (hi -> high nibble, lo -> low
 // nibble), round to nearest even, saturating to +-6.
@@ -522,6 +554,29 @@ __device__ __forceinline__ float2 f32x2_mul(float a, float b, float m) {
         "mov.b64 {%0, %1}, z;\n\t}"
         : "=f"(c.x), "=f"(c.y) : "f"(a), "f"(b), "f"(m));
     return c;
+}
+
+// acc += p * s and p *= s on a pair of FP32 lanes (round to nearest even per lane).
+__device__ __forceinline__ void f32x2_fma(uint64_t& acc, uint64_t p, uint64_t s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(p), "l"(s));
+}
+
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t p, uint64_t s) {
+    uint64_t o;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(p), "l"(s));
+    return o;
+}
+
+__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
+    uint64_t o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(lo), "f"(hi));
+    return o;
+}
+
+__device__ __forceinline__ float2 f32x2_unpack(uint64_t v) {
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(v));
+    return o;
 }
 
 // Two FP32 -> two E4M3 codes in 16 bits (hi -> bits 15:8, lo -> bits 7:0),
