@@ -31,8 +31,27 @@ struct GatedBwdParams {
     unsigned int* status;
 };
 
-// sigma(g); exp overflows to infinity for g < -88, which gives 0.
-__device__ __forceinline__ float sigmoid_f32(float g) { return __frcp_rn(__fadd_rn(1.0f, __expf(-g))); }
+// sigma(g) = 1 / (1 + e), e = exp(-g), within about two units: e = 2^hi (1 + lo ln 2)
+// with hi + lo = -g log2(e) carried in two floats, so that a large |g| costs no
+// precision.  e overflows to infinity for g < -88, which gives 0.
+struct Sigmoid {
+    float s, one_minus;         // sigma(g), 1 - sigma(g)
+};
+
+__device__ __forceinline__ float exp_neg(float g) {
+    const float hi = __fmul_rn(g, -1.4426950216f);
+    const float lo = __fmaf_rn(g, -1.9259630e-8f, __fmaf_rn(g, -1.4426950216f, -hi));
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(hi));
+    return fabsf(hi) < 126.0f ? __fmaf_rn(e, __fmul_rn(lo, 0.6931471806f), e) : e;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return __frcp_rn(__fadd_rn(1.0f, exp_neg(g))); }
+
+__device__ __forceinline__ Sigmoid sigmoid_both(float g) {
+    const float e = exp_neg(g), s = __frcp_rn(__fadd_rn(1.0f, e));
+    return {s, e > 1e30f ? 1.0f : __fmul_rn(e, s)};
+}
 
 __device__ __forceinline__ uint2 fp8_codes8(const float* v, const float (&f)[8]) {
     return make_uint2(cvt_e4m3x4(v[0] * f[0], v[1] * f[1], v[2] * f[2], v[3] * f[3]),
@@ -73,10 +92,11 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
                 return __uint_as_float((e & 1) ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
             };
             const float dh = pick(wh), gate = pick(wg), up = pick(wu);
-            const float sig = sigmoid_f32(gate), silu = gate * sig;
-            d[0][i][e] = dh * up * (sig * __fmaf_rn(gate, 1.0f - sig, 1.0f));
-            d[1][i][e] = dh * silu;
-            d[2][i][e] = silu * up;
+            const Sigmoid sg = sigmoid_both(gate);
+            // products of two BF16 values are exact in FP32: they come first
+            d[0][i][e] = __fmul_rn(__fmul_rn(dh, up), __fmul_rn(sg.s, __fmaf_rn(gate, sg.one_minus, 1.0f)));
+            d[1][i][e] = __fmul_rn(__fmul_rn(dh, gate), sg.s);
+            d[2][i][e] = __fmul_rn(__fmul_rn(gate, up), sg.s);
         }
     }
     // row-wise: dG and dU

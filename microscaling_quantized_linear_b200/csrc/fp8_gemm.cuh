@@ -10,7 +10,7 @@
 //
 // The scales are FP32, so the tensor core cannot apply them (its own block
 // scales are powers of two): each block's sum is taken by four MMAs into tensor
-// memory, and 16 epilogue warps read it, multiply by the scales and add it to
+// memory, and 8 epilogue warps read it, multiply by the scales and add it to
 // the FP32 total in their registers, while the MMAs of the next block fill the
 // other half of tensor memory (2 x 256 columns).
 //
@@ -22,8 +22,10 @@
 // the contiguous one (wgrad's, dgrad's weight) are staged as they lie in memory,
 // 128 of the contracted axis x 128 contiguous bytes, and read "MN-major" by the
 // MMA: no transposed copies.
-// Warps 0-15: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 and
-// 64 columns; 16: tile loads; 17: MMAs (in the leader CTA) and tensor memory.
+// Warps 0-7: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 and
+// 128 columns; 8: tile loads; 9 and 10: MMAs (in the leader CTA), each of every
+// other block, that is of one half of tensor memory: the tensor pipe queues
+// little, and while one warp goes through its barriers the other's MMAs run.
 // Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
 #pragma once
 #include <cstdint>
@@ -58,19 +60,21 @@ struct Fp8PairCfg {
     static constexpr bool A_MN = OP == kFp8Wgrad;                       // A's contiguous axis is its row axis
     static constexpr bool B_MN = OP == kFp8Wgrad || OP == kFp8Dgrad;
     static constexpr bool SB_COL = OP == kFp8Wgrad;                     // one B scale per column
-    static constexpr int EPI_WARPS = 16;
+    static constexpr int EPI_WARPS = 8;
     static constexpr int LOAD_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
-    static constexpr int THREADS = 32 * (EPI_WARPS + 2);
+    static constexpr int THREADS = 32 * (EPI_WARPS + 4);                // three warpgroups
+    // registers a thread: 384 x 168 at launch, shared out 256 x 224 + 128 x 56
+    static constexpr int EPI_REGS = 224, OTHER_REGS = 56;
+    static_assert(32 * EPI_WARPS * EPI_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
     static constexpr int TILE_BYTES = 128 * 128;                        // 128 rows x 128 bytes
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;                  // A and B tile of one CTA
-    static constexpr int STAGING = 32 * 64;                             // per epilogue warp
-    static constexpr int SB_BYTES = SB_COL ? EPI_WARPS * 2 * 256 : 0;   // per warp, two blocks of 64 scales
-    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 2 * 128 * 16 : 0;
+    static constexpr int STAGES = 6;
+    static constexpr int CHUNK_BUFS = SB_COL ? 1 : 2;                   // staging chunks of 32 rows x 64 bytes per epilogue warp
+    static constexpr int STAGING = CHUNK_BUFS * 32 * 64;
+    static constexpr int SB_BYTES = SB_COL ? EPI_WARPS * 2 * 512 : 0;   // per warp, two blocks of 128 scales
+    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 128 * 8 : 0;
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_LIMIT = 232448;
-    static constexpr int FIXED = 1024 + BAR_BYTES + EPI_WARPS * STAGING + SB_BYTES + AMAX_BYTES;
-    static constexpr int FIT = (SMEM_LIMIT - FIXED) / STAGE_BYTES;
-    static constexpr int STAGES = FIT > 6 ? 6 : FIT;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_SB = OFF_STAGING + EPI_WARPS * STAGING;
     static constexpr int OFF_AMAX = OFF_SB + SB_BYTES;
@@ -81,8 +85,8 @@ struct Fp8PairCfg {
                                       ((256u >> 3) << 17) | ((256u >> 4) << 24);
     // K step of 32 within a stage: 32 bytes along a row, or 32 rows of 128 bytes
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
-    static_assert(STAGES >= 4 && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
-    static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barriers");
+    static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+    static_assert((2 * STAGES + 6) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
 // Bounded wait of the pipeline: gives up after limit_ns or when *abort is set.
@@ -129,21 +133,24 @@ __device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src,
 }
 
 // Writes one 32-row x 64-byte chunk (v: this thread's row) through the warp's
-// staging buffer: 64-byte swizzle, then a tensor-map store, or an addition.
-__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[16], uint8_t* staging, const CUtensorMap* map, int32_t c,
-                                                int32_t r, uint32_t lane, bool add) {
+// BUFS staging buffers in turn: 64-byte swizzle, then a tensor-map store, or an
+// addition.
+template <int BUFS>
+__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[16], uint8_t* staging, uint32_t& chunk,
+                                                const CUtensorMap* map, int32_t c, int32_t r, uint32_t lane, bool add) {
     const uint32_t swz = (lane >> 1) & 3;
-    if (lane == 0) bulk_wait_group_read<0>();            // the previous store has read the buffer
+    uint8_t* buf = staging + (chunk++ % BUFS) * 2048;
+    if (lane == 0) bulk_wait_group_read<BUFS - 1>();     // the store that used this buffer last has read it
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(staging + lane * 64 + 16 * ((uint32_t)i ^ swz)) =
+        *reinterpret_cast<uint4*>(buf + lane * 64 + 16 * ((uint32_t)i ^ swz)) =
             make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        if (add) tma_reduce_add_2d(map, smem_u32(staging), c, r);
-        else tma_store_2d(map, smem_u32(staging), c, r);
+        if (add) tma_reduce_add_2d(map, smem_u32(buf), c, r);
+        else tma_store_2d(map, smem_u32(buf), c, r);
         bulk_commit_group();
     }
 }
@@ -169,8 +176,8 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     const uint32_t empty0 = full0 + 8 * C::STAGES;
     const uint32_t tfull0 = empty0 + 8 * C::STAGES;
     const uint32_t tempty0 = tfull0 + 16;
-    const uint32_t drain = tempty0 + 16;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+    const uint32_t drain0 = tempty0 + 16;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 6);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* never = abort_flag + 1;
 
@@ -185,8 +192,8 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 2 * C::EPI_WARPS);
+            mbar_init(drain0 + 8 * b, 1);
         }
-        mbar_init(drain, 1);
         *abort_flag = 0;
         *never = 0;
         fence_mbarrier_init();
@@ -213,68 +220,71 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         atomicOr(p.status, kStatusTimeout);
     };
 
-    if (warp == C::LOAD_WARP) {
-        // ---------------------------------------------------------- tile loads (both CTAs)
-        if (PLAIN_A || lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            // the plain copies of iteration j are complete: publish them to the leader's MMAs
-            const auto publish = [&](uint32_t j) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
-            };
-            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
-                const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
-                const uint32_t cb = tile / p.row_tiles;
-                const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
-                for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-                    const int32_t k0 = (int32_t)(t * 128);
-                    if (lane == 0) {
-                        const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
-                        if (rank == 0)
-                            mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
-                        if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
-                        tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
-                    }
-                    if (PLAIN_A) {
-                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
-                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
-                        cp_async_commit();
-                        if (it > 0) {
-                            cp_async_wait<1>();
-                            publish(it - 1);
+    if (warp >= C::EPI_WARPS) {
+        regs_dec<C::OTHER_REGS>();
+        if (warp == C::LOAD_WARP) {
+            // ---------------------------------------------------------- tile loads (both CTAs)
+            if (PLAIN_A || lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                // the plain copies of iteration j are complete: publish them to the leader's MMAs
+                const auto publish = [&](uint32_t j) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
+                };
+                for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                    const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
+                    const uint32_t cb = tile / p.row_tiles;
+                    const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
+                    for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                        const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                        if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+                        const int32_t k0 = (int32_t)(t * 128);
+                        if (lane == 0) {
+                            const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
+                            if (rank == 0)
+                                mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
+                            if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
+                            tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
+                        }
+                        if (PLAIN_A) {
+                            if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
+                            else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
+                            cp_async_commit();
+                            if (it > 0) {
+                                cp_async_wait<1>();
+                                publish(it - 1);
+                            }
                         }
                     }
                 }
+                if (PLAIN_A && it > 0) {
+                    cp_async_wait<0>();
+                    publish(it - 1);
+                }
+                if (lane == 0) {
+                    if (!ok) gave_up();
+                    // Neither CTA leaves while a load it issued may be in flight: the leader's
+                    // barriers count both CTAs' bytes; the peer learns of its own through the
+                    // commits of the MMAs that consumed them.
+                    for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                        fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never, kFp8WaitNs);
+                }
             }
-            if (PLAIN_A && it > 0) {
-                cp_async_wait<0>();
-                publish(it - 1);
-            }
-            if (lane == 0) {
-                if (!ok) gave_up();
-                // Neither CTA leaves while a load it issued may be in flight: the leader's
-                // barriers count both CTAs' bytes; the peer learns of its own through the
-                // commits of the MMAs that consumed them.
-                for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                    fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never, kFp8WaitNs);
-            }
-        }
-    } else if (warp == C::MMA_WARP) {
-        // ---------------------------------------------------------- MMAs (leader)
-        if (lane == 0 && rank == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
-                for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                    const uint32_t s = it % C::STAGES, b = it & 1, use = it >> 1;
+        } else if (warp == C::MMA_WARP || warp == C::MMA_WARP + 1) {
+            // ---------------------------------------------------------- MMAs (leader), one warp per accumulator half
+            if (lane == 0 && rank == 0) {
+                const uint32_t b = warp - C::MMA_WARP;
+                const uint32_t my_tiles = num_tiles > pair ? (num_tiles - pair + npairs - 1) / npairs : 0;
+                const uint32_t total = my_tiles * blocks;
+                bool ok = true;
+                for (uint32_t it = b; it < total; it += 2) {
+                    const uint32_t s = it % C::STAGES, use = it >> 1;
                     if ((use > 0 && !fp8_wait(tempty0 + 8 * b, (use - 1) & 1, abort_flag, p.wait_ns)) ||
                         !fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns)) {
                         ok = false;
@@ -282,195 +292,208 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     }
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-#pragma unroll
+    #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
                         tc_mma_f8_pair(tmem + b * 256, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
                                        smem_desc(st + C::TILE_BYTES + k * C::B_STEP, 1024, 1024, 2), C::IDESC, k != 0);
-                    tc_commit_pair_mc(empty0 + 8 * s, 0x3);
                     tc_commit_pair_mc(tfull0 + 8 * b, 0x3);
+                    tc_commit_pair_mc(empty0 + 8 * s, 0x3);
                 }
+                if (!ok) gave_up();
+                tc_commit_pair(drain0 + 8 * b);
+                fp8_wait(drain0 + 8 * b, 0, never, kFp8WaitNs);
             }
-            if (!ok) gave_up();
-            tc_commit_pair(drain);
-            fp8_wait(drain, 0, never, kFp8WaitNs);
         }
     } else {
+        regs_inc<C::EPI_REGS>();
         // ---------------------------------------------------------- epilogue (both CTAs)
         const uint32_t q = warp & 3, g = warp >> 2;
         uint8_t* staging = smem + C::OFF_STAGING + warp * C::STAGING;
-        float* s_sb = reinterpret_cast<float*>(smem + C::OFF_SB + warp * 512);
-        float* s_amax = reinterpret_cast<float*>(smem + C::OFF_AMAX);
-        // this warp's two chunks of 32 columns of the 256 (gated: of gate and of up)
-        const uint32_t col0 = OP == kFp8Gated ? 32 * g : 64 * g;
-        const uint32_t col1 = OP == kFp8Gated ? 128 + 32 * g : 64 * g + 32;
+        float* s_sb = reinterpret_cast<float*>(smem + C::OFF_SB + warp * 1024);
+        uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
+        // chunk j (32 columns) of this warp starts at tile column 128 g + 32 j; gated: 64 g + 32 j of
+        // gate (j = 0, 1), and the same columns of up (j = 2, 3)
+        const auto chunk_col = [&](uint32_t j) { return OP == kFp8Gated ? 64 * g + 32 * (j & 1) + 128 * (j >> 1) : 128 * g + 32 * j; };
         const uint32_t lanes = tmem + ((32 * q) << 16);
-        uint32_t it = 0, tiles_done = 0;
+        const uint32_t cblocks = (p.C + 127) / 128;
+        const uint64_t sa_n = (uint64_t)blocks * p.R, sbc_n = (uint64_t)blocks * p.C;
+        uint32_t it = 0, chunk = 0;
         bool ok = true;
-        for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs, ++tiles_done) {
+        for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
             const uint32_t rw = (tile % p.row_tiles) * 256 + 128 * rank + 32 * q;      // the warp's first row
             const uint32_t cb = tile / p.row_tiles;
             const uint32_t r = rw + lane, rc = min(r, p.R - 1);
             const uint32_t n0 = cb * (OP == kFp8Gated ? 128 : 256);                    // the tile's first column
-            const uint32_t cblocks = (p.C + 127) / 128;
-            // scales of block t: the row's, and the columns' (one per 128, or one per column)
+            // scales of block t, read two blocks ahead: the row's, and the columns' (one per 128, or one per column)
             const float* sap = p.sa + rc;
-            const float* sbp0;
-            const float* sbp1;
-            uint32_t sb_step = 1;
+            const float *sbp0 = p.sb, *sbp1 = p.sb;
+            const uint32_t sb_step = OP == kFp8Dgrad ? cblocks : 1;
             if (OP == kFp8Gated) {
                 sbp0 = p.sb + (size_t)cb * blocks;
                 sbp1 = p.sb + (size_t)(cb + cblocks) * blocks;
-            } else {
-                const uint32_t nb = min((n0 + col0) / 128, cblocks - 1);
-                sbp0 = sbp1 = OP == kFp8Dgrad ? p.sb + nb : p.sb + (size_t)nb * blocks;
-                if (OP == kFp8Dgrad) sb_step = cblocks;
+            } else if (!C::SB_COL) {
+                const uint32_t nb = min(n0 / 128 + g, cblocks - 1);
+                sbp0 = OP == kFp8Dgrad ? p.sb + nb : p.sb + (size_t)nb * blocks;
             }
-            const uint64_t sa_n = (uint64_t)blocks * p.R, sbc_n = (uint64_t)blocks * p.C;
             const auto row_scale = [&](uint32_t t) {
                 return t < blocks && in_bounds((uint64_t)t * p.R + rc, 1, sa_n, p.status) ? __ldg(sap + (size_t)t * p.R) : 0.0f;
             };
-            // wgrad: this lane's two of the warp's 64 column scales (C is even)
-            const uint32_t sc = n0 + col0 + 2 * lane;
+            const auto tile_scale = [&](const float* sb, uint32_t t) { return t < blocks ? __ldg(sb + (size_t)t * sb_step) : 0.0f; };
+            // wgrad: this lane's four of the warp's 128 column scales (C is a multiple of 16)
+            const uint32_t sc = n0 + 128 * g + 4 * lane;
             const auto col_scales = [&](uint32_t t) {
-                if (t < blocks && sc < p.C && in_bounds((uint64_t)t * p.C + sc, 2, sbc_n, p.status))
-                    return __ldg(reinterpret_cast<const float2*>(p.sb + (size_t)t * p.C + sc));
-                return make_float2(0.0f, 0.0f);
+                if (t < blocks && sc < p.C && in_bounds((uint64_t)t * p.C + sc, 4, sbc_n, p.status))
+                    return __ldg(reinterpret_cast<const float4*>(p.sb + (size_t)t * p.C + sc));
+                return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             };
-            uint64_t acc0[16] = {}, acc1[16] = {};
+            uint64_t acc[4][16] = {};
             float sa_a = row_scale(0), sa_b = row_scale(1);
             float b0_a = 0, b0_b = 0, b1_a = 0, b1_b = 0;
-            float2 bc_a, bc_b;
+            float4 bc_a, bc_b;
             if (C::SB_COL) {
                 bc_a = col_scales(0);
                 bc_b = col_scales(1);
             } else {
-                b0_a = __ldg(sbp0);
-                b0_b = blocks > 1 ? __ldg(sbp0 + sb_step) : 0.0f;
+                b0_a = tile_scale(sbp0, 0);
+                b0_b = tile_scale(sbp0, 1);
                 if (OP == kFp8Gated) {
-                    b1_a = __ldg(sbp1);
-                    b1_b = blocks > 1 ? __ldg(sbp1 + sb_step) : 0.0f;
+                    b1_a = tile_scale(sbp1, 0);
+                    b1_b = tile_scale(sbp1, 1);
                 }
             }
             for (uint32_t t = 0; t < blocks; ++t, ++it) {
                 const uint32_t b = it & 1;
-                const float sa = sa_a, b0 = b0_a, b1 = b1_a;
-                sa_a = sa_b;
-                sa_b = row_scale(t + 2);
+                float f0 = sa_a, f1;
                 if (C::SB_COL) {
-                    *reinterpret_cast<float2*>(s_sb + 64 * b + 2 * lane) = bc_a;
+                    *reinterpret_cast<float4*>(s_sb + 128 * b + 4 * lane) = bc_a;
                     bc_a = bc_b;
                     bc_b = col_scales(t + 2);
                     __syncwarp();
+                    f1 = f0;
                 } else {
+                    f1 = OP == kFp8Gated ? __fmul_rn(sa_a, b1_a) : 0.0f;
+                    f0 = __fmul_rn(sa_a, b0_a);
+                    if (OP != kFp8Gated) f1 = f0;
                     b0_a = b0_b;
-                    b0_b = t + 2 < blocks ? __ldg(sbp0 + (size_t)(t + 2) * sb_step) : 0.0f;
+                    b0_b = tile_scale(sbp0, t + 2);
                     if (OP == kFp8Gated) {
                         b1_a = b1_b;
-                        b1_b = t + 2 < blocks ? __ldg(sbp1 + (size_t)(t + 2) * sb_step) : 0.0f;
+                        b1_b = tile_scale(sbp1, t + 2);
                     }
                 }
-                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, b0);
-                const float f1 = OP == kFp8Gated ? __fmul_rn(sa, b1) : f0;
+                sa_a = sa_b;
+                sa_b = row_scale(t + 2);
                 const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
                 if (!fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const auto add = [&](const uint32_t (&v)[32], uint64_t (&acc)[16], uint64_t s, const float* sb) {
+                const auto add = [&](const uint32_t (&v)[32], int j) {
+                    const uint64_t s = j < 2 ? s0 : s1;
+                    const float4* sb = reinterpret_cast<const float4*>(s_sb + 128 * b + 32 * j);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint64_t x = f32x2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if (C::SB_COL) x = f32x2_mul(x, *reinterpret_cast<const uint64_t*>(sb + 2 * i));
-                        f32x2_fma(acc[i], x, s);
+                    for (int i = 0; i < 8; ++i) {
+                        uint64_t x = f32x2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
+                        uint64_t y = f32x2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                        if (C::SB_COL) {
+                            const float4 c = sb[i];
+                            x = f32x2_mul(x, f32x2_pack(c.x, c.y));
+                            y = f32x2_mul(y, f32x2_pack(c.z, c.w));
+                        }
+                        f32x2_fma(acc[j][2 * i], x, s);
+                        f32x2_fma(acc[j][2 * i + 1], y, s);
                     }
                 };
-                uint32_t v[32];
-                tc_ld_32x32b_x32(lanes + b * 256 + col0, v);
-                tc_wait_ld();
-                add(v, acc0, s0, s_sb + 64 * b);
-                tc_ld_32x32b_x32(lanes + b * 256 + col1, v);
-                tc_wait_ld();
+                // a chunk's load runs while the chunk before it is added
+                uint32_t v[2][32];
+                tc_ld_32x32b_x32(lanes + b * 256 + chunk_col(0), v[0]);
+                tc_wait_ld(v[0]);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    tc_ld_32x32b_x32(lanes + b * 256 + chunk_col(j + 1), v[(j + 1) & 1]);
+                    add(v[j & 1], j);
+                    tc_wait_ld(v[(j + 1) & 1]);
+                }
                 tc_fence_before();
                 __syncwarp();
                 // the loads have returned, and the signal publishes no memory writes
                 if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(tempty0 + 8 * b, 0));
-                add(v, acc1, s1, s_sb + 64 * b + 32);
+                add(v[1], 3);
             }
             if (!ok) break;
             if (OP == kFp8Gated) {
                 const uint64_t h_n = (uint64_t)p.R * p.C;
                 if (p.save && rw < p.R) {
-                    uint32_t o[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = f32x2_unpack(acc0[i]);
-                        o[i] = bf16x2_of(x.x, x.y);
-                    }
-                    fp8_store_chunk(o, staging, &tmap_out, (int32_t)(n0 + col0), (int32_t)rw, lane, false);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = f32x2_unpack(acc1[i]);
-                        o[i] = bf16x2_of(x.x, x.y);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = f32x2_unpack(acc[j][i]);
+                            o[i] = bf16x2_of(x.x, x.y);
+                        }
+                        fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)(n0 + (j >> 1) * p.C + 64 * g + 32 * (j & 1)),
+                                        (int32_t)rw, lane, false);
                     }
-                    fp8_store_chunk(o, staging, &tmap_out, (int32_t)(p.C + n0 + col0), (int32_t)rw, lane, false);
                 }
-                float h[32];
+                float h[64];
                 uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 x = f32x2_unpack(acc0[i]), u = f32x2_unpack(acc1[i]);
+                for (int i = 0; i < 32; ++i) {
+                    const float2 x = f32x2_unpack(acc[i >> 4][i & 15]), u = f32x2_unpack(acc[2 + (i >> 4)][i & 15]);
                     h[2 * i] = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
                     h[2 * i + 1] = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
                     m = max(m, max(abs_bits(h[2 * i]), abs_bits(h[2 * i + 1])));
                 }
-                // the block of 128 columns is shared by the four warps of this lane quarter
-                uint32_t* am = reinterpret_cast<uint32_t*>(s_amax) + (tiles_done & 1) * 512 + (32 * q + lane) * 4;
+                // the block of 128 columns is shared by the two warps of this lane quarter
+                uint32_t* am = s_amax + (32 * q + lane) * 2;
                 am[g] = m;
-                named_barrier_sync(1 + q, 128);
-                const uint4 m4 = *reinterpret_cast<const uint4*>(am);
-                m = max(max(m4.x, m4.y), max(m4.z, m4.w));
+                named_barrier_sync(1 + q, 64);
+                m = max(m, am[g ^ 1]);
+                named_barrier_sync(1 + q, 64);           // read before the next tile's is written
                 if (r < p.R) {
                     const Fp8Scale s = fp8_block_scale(m, p.status);
-                    const uint64_t at = (uint64_t)r * p.C + n0 + col0;
-                    uint32_t w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w[i] = cvt_e4m3x4(h[4 * i] * s.factor, h[4 * i + 1] * s.factor, h[4 * i + 2] * s.factor,
-                                          h[4 * i + 3] * s.factor);
-                    if (in_bounds(at, 32, h_n, p.status)) {
+                    const uint64_t at = (uint64_t)r * p.C + n0 + 64 * g;
+                    if (in_bounds(at, 64, h_n, p.status)) {
                         uint4* d = reinterpret_cast<uint4*>(p.h_codes + at);
-                        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float* x = h + 16 * i + 4 * e;
+                                w[e] = cvt_e4m3x4(x[0] * s.factor, x[1] * s.factor, x[2] * s.factor, x[3] * s.factor);
+                            }
+                            d[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
                     if (g == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
                         p.h_scales[(size_t)cb * p.R + r] = s.scale;
                 }
             } else if (rw < p.R) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t c = n0 + (half ? col1 : col0);
-                    const uint64_t(&acc)[16] = half ? acc1 : acc0;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t c = n0 + 128 * g + 32 * j;
                     if (c >= p.C) continue;
+                    uint32_t o[16];
                     if (OP == kFp8Wgrad) {
-                        // 16 FP32 columns a chunk
-                        uint32_t o[16];
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
+                        for (int part = 0; part < 2; ++part) {          // 16 FP32 columns a chunk
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float2 x = f32x2_unpack(acc[8 * part + i]);
+                                const float2 x = f32x2_unpack(acc[j][8 * part + i]);
                                 o[2 * i] = __float_as_uint(x.x);
                                 o[2 * i + 1] = __float_as_uint(x.y);
                             }
                             if (c + 16 * part < p.C)
-                                fp8_store_chunk(o, staging, &tmap_out, (int32_t)(c + 16 * part), (int32_t)rw, lane, p.accumulate);
+                                fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)(c + 16 * part), (int32_t)rw, lane,
+                                                p.accumulate);
                         }
                     } else {
-                        uint32_t o[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float2 x = f32x2_unpack(acc[i]);
+                            float2 x = f32x2_unpack(acc[j][i]);
                             // C is a multiple of 8, so a pair of columns is inside or outside
                             if (OP == kFp8Linear && p.bias && c + 2 * i < p.C) {
                                 const __nv_bfloat162 bb = *reinterpret_cast<const __nv_bfloat162*>(p.bias + c + 2 * i);
@@ -479,7 +502,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                             }
                             o[i] = bf16x2_of(x.x, x.y);
                         }
-                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)c, (int32_t)rw, lane, false);
+                        fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)c, (int32_t)rw, lane, false);
                     }
                 }
             }
