@@ -46,10 +46,19 @@ __device__ __forceinline__ float exp_neg(float g) {
     return fabsf(hi) < 126.0f ? __fmaf_rn(e, __fmul_rn(lo, 0.6931471806f), e) : e;
 }
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return __frcp_rn(__fadd_rn(1.0f, exp_neg(g))); }
+// 1 / (1 + e) to about half a unit: the approximate reciprocal and one Newton step
+// (not where 1 + e nears the largest floats, whose reciprocal needs no more).
+__device__ __forceinline__ float sigmoid_of_exp(float e) {
+    const float d = __fadd_rn(1.0f, e);
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return e < 1e30f ? __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r) : r;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return sigmoid_of_exp(exp_neg(g)); }
 
 __device__ __forceinline__ Sigmoid sigmoid_both(float g) {
-    const float e = exp_neg(g), s = __frcp_rn(__fadd_rn(1.0f, e));
+    const float e = exp_neg(g), s = sigmoid_of_exp(e);
     return {s, e > 1e30f ? 1.0f : __fmul_rn(e, s)};
 }
 

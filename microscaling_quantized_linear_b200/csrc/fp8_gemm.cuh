@@ -9,10 +9,9 @@
 // gated     linear onto gate and up; H = SiLU(gate) * up quantized row-wise
 //
 // The scales are FP32, so the tensor core cannot apply them (its own block
-// scales are powers of two): each block's sum is taken by four MMAs into tensor
-// memory, and 8 epilogue warps read it, multiply by the scales and add it to
-// the FP32 total in their registers, while the MMAs of the next block fill the
-// other half of tensor memory (2 x 256 columns).
+// scales are powers of two): each block's sum is taken by MMAs into tensor
+// memory, and 16 epilogue warps read it, multiply by the scales and add it to
+// the FP32 total in their registers while the MMAs go on.
 //
 // CTA pairs, one per two SMs, persistent over 256 x 256 output tiles (gated: 256
 // rows x 128 columns of H, gate's 128 columns and up's as one 256-wide B tile).
@@ -22,10 +21,21 @@
 // the contiguous one (wgrad's, dgrad's weight) are staged as they lie in memory,
 // 128 of the contracted axis x 128 contiguous bytes, and read "MN-major" by the
 // MMA: no transposed copies.
-// Warps 0-7: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 and
-// 128 columns; 8: tile loads; 9 and 10: MMAs (in the leader CTA), each of every
-// other block, that is of one half of tensor memory: the tensor pipe queues
-// little, and while one warp goes through its barriers the other's MMAs run.
+//
+// A block is two units, h = 0 and 1: the MMA of unit h reads rows [64 h, 64 h +
+// 64) of each CTA's B tile, so its 128 accumulator columns are tile columns
+// 64 h .. + 63 and 128 + 64 h .. + 63.  Tensor memory holds four units, two of
+// each h.  From an accumulator's completion to the MMA that may overwrite it lie
+// three hand-overs between threads (about 300 cycles each) and the drain; with
+// two 256-wide accumulators the tensor pipe stood idle for half of that time
+// (4608 x 12288 x 4096: 242 us against LATER us with units).
+// Warps 0-15: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31,
+// columns 64 (w / 8) .. + 63 of unit (w / 4) % 2 (gated: 32 of gate and of up);
+// 16: tile loads; 17 and 18: MMAs (in the leader CTA) of unit 0 and of unit 1:
+// the tensor pipe queues little, and while one warp goes through its barriers
+// the other's MMAs run; 19: scales, into a ring of eight blocks.  They are loaded
+// as far ahead as the tiles: L2 answers after some 2,000 cycles while the tiles
+// stream in, and reading them two blocks ahead in the epilogue cost 80 us of 298.
 // Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
 #pragma once
 #include <cstdint>
@@ -60,33 +70,35 @@ struct Fp8PairCfg {
     static constexpr bool A_MN = OP == kFp8Wgrad;                       // A's contiguous axis is its row axis
     static constexpr bool B_MN = OP == kFp8Wgrad || OP == kFp8Dgrad;
     static constexpr bool SB_COL = OP == kFp8Wgrad;                     // one B scale per column
-    static constexpr int EPI_WARPS = 8;
-    static constexpr int LOAD_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
-    static constexpr int THREADS = 32 * (EPI_WARPS + 4);                // three warpgroups
-    // registers a thread: 384 x 168 at launch, shared out 256 x 224 + 128 x 56
-    static constexpr int EPI_REGS = 224, OTHER_REGS = 56;
-    static_assert(32 * EPI_WARPS * EPI_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
+    static constexpr int EPI_WARPS = 16;
+    static constexpr int LOAD_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1, SCALE_WARP = EPI_WARPS + 3;
+    static constexpr int THREADS = 32 * (EPI_WARPS + 4);                // five warpgroups
+    // registers a thread: 640 x 96 at launch, shared out 512 x 112 + 128 x 32
+    static constexpr int EPI_REGS = 112, OTHER_REGS = 32;
+    static_assert(32 * EPI_WARPS * EPI_REGS + 128 * OTHER_REGS <= THREADS * 96, "register split");
     static constexpr int TILE_BYTES = 128 * 128;                        // 128 rows x 128 bytes
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;                  // A and B tile of one CTA
-    static constexpr int STAGES = 6;
-    static constexpr int CHUNK_BUFS = SB_COL ? 1 : 2;                   // staging chunks of 32 rows x 64 bytes per epilogue warp
-    static constexpr int STAGING = CHUNK_BUFS * 32 * 64;
-    static constexpr int SB_BYTES = SB_COL ? EPI_WARPS * 2 * 512 : 0;   // per warp, two blocks of 128 scales
-    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 128 * 8 : 0;
+    static constexpr int STAGES = 5;
+    static constexpr int STAGING = 32 * 64;                             // per epilogue warp: one chunk
+    // scale slot of a block: 128 row scales, then 256 column scales or the two tile scales
+    static constexpr int SLOTS = 8;
+    static constexpr int SLOT_BYTES = 512 + (SB_COL ? 1024 : 16);
+    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 3 * 128 * 4 : 0;
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_LIMIT = 232448;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
-    static constexpr int OFF_SB = OFF_STAGING + EPI_WARPS * STAGING;
-    static constexpr int OFF_AMAX = OFF_SB + SB_BYTES;
-    static constexpr int OFF_BAR = OFF_AMAX + AMAX_BYTES;
+    static constexpr int OFF_AMAX = OFF_STAGING + EPI_WARPS * STAGING;
+    static constexpr int OFF_SCALE = OFF_AMAX + AMAX_BYTES;
+    static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
     static constexpr int SMEM_BYTES = OFF_BAR + BAR_BYTES + 1024;
     // instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 x E4M3, major-ness, N / 8, M / 16
     static constexpr uint32_t IDESC = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
-                                      ((256u >> 3) << 17) | ((256u >> 4) << 24);
+                                      ((128u >> 3) << 17) | ((256u >> 4) << 24);
     // K step of 32 within a stage: 32 bytes along a row, or 32 rows of 128 bytes
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
+    static constexpr uint32_t B_UNIT = B_MN ? 64 : 64 * 128;            // from unit 0's B to unit 1's
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
-    static_assert((2 * STAGES + 6) * 8 + 16 <= BAR_BYTES, "barriers");
+    static_assert((2 * STAGES + 10 + SLOTS) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
 // Bounded wait of the pipeline: gives up after limit_ns or when *abort is set.
@@ -133,14 +145,11 @@ __device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src,
 }
 
 // Writes one 32-row x 64-byte chunk (v: this thread's row) through the warp's
-// BUFS staging buffers in turn: 64-byte swizzle, then a tensor-map store, or an
-// addition.
-template <int BUFS>
-__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[16], uint8_t* staging, uint32_t& chunk,
-                                                const CUtensorMap* map, int32_t c, int32_t r, uint32_t lane, bool add) {
+// staging buffer: 64-byte swizzle, then a tensor-map store, or an addition.
+__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[16], uint8_t* buf, const CUtensorMap* map, int32_t c,
+                                                int32_t r, uint32_t lane, bool add) {
     const uint32_t swz = (lane >> 1) & 3;
-    uint8_t* buf = staging + (chunk++ % BUFS) * 2048;
-    if (lane == 0) bulk_wait_group_read<BUFS - 1>();     // the store that used this buffer last has read it
+    if (lane == 0) bulk_wait_group_read<0>();            // the previous store has read the buffer
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -169,15 +178,17 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     // full[s]:   the stage's tiles of both CTAs landed (leader's barrier)
-    // empty[s]:  the stage's MMAs completed (commit multicast to both CTAs)
-    // tfull[b]:  accumulator half b holds a block's sums (both CTAs)
-    // tempty[b]: both CTAs' epilogue warps have read half b (leader's barrier)
+    // empty[s]:  both units' MMAs of the stage completed (commits multicast to both CTAs)
+    // tfull[b]:  accumulator b (of unit b % 2) holds a block's sums (both CTAs)
+    // tempty[b]: both CTAs' epilogue warps have read accumulator b (leader's barrier)
+    // sfull[i]:  scale slot i holds a block's scales (each lane of the scale warp arrives)
     const uint32_t full0 = smem_u32(bars);
     const uint32_t empty0 = full0 + 8 * C::STAGES;
     const uint32_t tfull0 = empty0 + 8 * C::STAGES;
-    const uint32_t tempty0 = tfull0 + 16;
-    const uint32_t drain0 = tempty0 + 16;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 6);
+    const uint32_t tempty0 = tfull0 + 32;
+    const uint32_t drain0 = tempty0 + 32;
+    const uint32_t sfull0 = drain0 + 16;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 10 + C::SLOTS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* never = abort_flag + 1;
 
@@ -187,13 +198,15 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full0 + 8 * s, PLAIN_A ? 3 : 1);
-            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 2);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, 2 * C::EPI_WARPS);
-            mbar_init(drain0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, C::EPI_WARPS);      // half of each CTA's epilogue warps
         }
+        mbar_init(drain0, 1);
+        mbar_init(drain0 + 8, 1);
+        for (int i = 0; i < C::SLOTS; ++i) mbar_init(sfull0 + 8 * i, 32);
         *abort_flag = 0;
         *never = 0;
         fence_mbarrier_init();
@@ -277,123 +290,124 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 }
             }
         } else if (warp == C::MMA_WARP || warp == C::MMA_WARP + 1) {
-            // ---------------------------------------------------------- MMAs (leader), one warp per accumulator half
+            // ---------------------------------------------------------- MMAs (leader), one warp per unit
             if (lane == 0 && rank == 0) {
-                const uint32_t b = warp - C::MMA_WARP;
+                const uint32_t h = warp - C::MMA_WARP;
                 const uint32_t my_tiles = num_tiles > pair ? (num_tiles - pair + npairs - 1) / npairs : 0;
                 const uint32_t total = my_tiles * blocks;
                 bool ok = true;
-                for (uint32_t it = b; it < total; it += 2) {
-                    const uint32_t s = it % C::STAGES, use = it >> 1;
-                    if ((use > 0 && !fp8_wait(tempty0 + 8 * b, (use - 1) & 1, abort_flag, p.wait_ns)) ||
-                        !fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns)) {
+                for (uint32_t it = 0; it < total; ++it) {
+                    const uint32_t s = it % C::STAGES, b = h + 2 * (it & 1), use = it >> 1;
+                    if (!fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns) ||
+                        (use > 0 && !fp8_wait(tempty0 + 8 * b, (use - 1) & 1, abort_flag, p.wait_ns))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-    #pragma unroll
+#pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        tc_mma_f8_pair(tmem + b * 256, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
-                                       smem_desc(st + C::TILE_BYTES + k * C::B_STEP, 1024, 1024, 2), C::IDESC, k != 0);
+                        tc_mma_f8_pair(tmem + b * 128, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
+                                       smem_desc(st + C::TILE_BYTES + h * C::B_UNIT + k * C::B_STEP, 1024, 1024, 2), C::IDESC,
+                                       k != 0);
                     tc_commit_pair_mc(tfull0 + 8 * b, 0x3);
                     tc_commit_pair_mc(empty0 + 8 * s, 0x3);
                 }
                 if (!ok) gave_up();
-                tc_commit_pair(drain0 + 8 * b);
-                fp8_wait(drain0 + 8 * b, 0, never, kFp8WaitNs);
+                tc_commit_pair(drain0 + 8 * h);
+                fp8_wait(drain0 + 8 * h, 0, never, kFp8WaitNs);
             }
+        } else if (warp == C::SCALE_WARP) {
+            // ---------------------------------------------------------- scales (both CTAs)
+            // Slot it % 8 held block it - 8.  The MMAs of block it - STAGES (whose completion is
+            // waited for) overwrote the accumulators of block it - STAGES - 2, so every epilogue warp
+            // had released those and, in order, was past block it - 8.
+            static_assert(C::STAGES + 2 <= C::SLOTS, "scale ring");
+            const uint32_t cblocks = (p.C + 127) / 128;
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const uint32_t r0 = (tile % p.row_tiles) * 256 + 128 * rank + lane, cb = tile / p.row_tiles;
+                const uint32_t nb = OP == kFp8Gated ? cb + (lane & 1) * cblocks : min(2 * cb + (lane & 1), cblocks - 1);
+                for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                    if (it >= (uint32_t)C::STAGES &&
+                        !fp8_wait(empty0 + 8 * (it % C::STAGES), (it / C::STAGES - 1) & 1, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t slot = smem_u32(smem + C::OFF_SCALE + (it % C::SLOTS) * C::SLOT_BYTES);
+                    const float* sa = p.sa + (size_t)t * p.R;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t r = r0 + 32 * i;
+                        const bool in = r < p.R && in_bounds((uint64_t)t * p.R + r, 1, (uint64_t)blocks * p.R, p.status);
+                        cp_async4_zfill(slot + 4 * (lane + 32 * i), in ? sa + r : p.sa, in ? 4 : 0);
+                    }
+                    if (C::SB_COL) {
+                        const float* sb = p.sb + (size_t)t * p.C;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {           // C is a multiple of 16
+                            const uint32_t c = cb * 256 + 4 * (lane + 32 * i);
+                            const bool in = c < p.C && in_bounds((uint64_t)t * p.C + c, 4, (uint64_t)blocks * p.C, p.status);
+                            cp_async16_zfill(slot + 512 + 16 * (lane + 32 * i), in ? sb + c : p.sb, in ? 16 : 0);
+                        }
+                    } else if (lane < 2) {
+                        const uint64_t at = OP == kFp8Dgrad ? (uint64_t)t * cblocks + nb : (uint64_t)nb * blocks + t;
+                        const bool in = in_bounds(at, 1, (uint64_t)blocks * (OP == kFp8Gated ? 2 : 1) * cblocks, p.status);
+                        cp_async4_zfill(slot + 512 + 4 * lane, in ? p.sb + at : p.sb, in ? 4 : 0);
+                    }
+                    cp_async_arrive(sfull0 + 8 * (it % C::SLOTS));
+                }
+            }
+            if (!ok && lane == 0) gave_up();
+            cp_async_commit();
+            cp_async_wait<0>();
         }
     } else {
         regs_inc<C::EPI_REGS>();
         // ---------------------------------------------------------- epilogue (both CTAs)
-        const uint32_t q = warp & 3, g = warp >> 2;
+        const uint32_t q = warp & 3, h = (warp >> 2) & 1, j2 = warp >> 3;
         uint8_t* staging = smem + C::OFF_STAGING + warp * C::STAGING;
-        float* s_sb = reinterpret_cast<float*>(smem + C::OFF_SB + warp * 1024);
         uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
-        // chunk j (32 columns) of this warp starts at tile column 128 g + 32 j; gated: 64 g + 32 j of
-        // gate (j = 0, 1), and the same columns of up (j = 2, 3)
-        const auto chunk_col = [&](uint32_t j) { return OP == kFp8Gated ? 64 * g + 32 * (j & 1) + 128 * (j >> 1) : 128 * g + 32 * j; };
+        if (OP == kFp8Gated) {
+            if (threadIdx.x < 384) s_amax[threadIdx.x] = 0;
+            named_barrier_sync(5, 32 * C::EPI_WARPS);
+        }
+        // the warp's 64 columns of the tile (gated: 32 of gate, and the same of up)
+        const uint32_t tcol = OP == kFp8Gated ? 64 * h + 32 * j2 : 128 * j2 + 64 * h;
+        // chunk j (16 columns) in the unit's accumulator
+        const auto chunk_col = [&](uint32_t j) { return OP == kFp8Gated ? 32 * j2 + 16 * (j & 1) + 64 * (j >> 1) : 64 * j2 + 16 * j; };
         const uint32_t lanes = tmem + ((32 * q) << 16);
         const uint32_t cblocks = (p.C + 127) / 128;
-        const uint64_t sa_n = (uint64_t)blocks * p.R, sbc_n = (uint64_t)blocks * p.C;
-        uint32_t it = 0, chunk = 0;
+        uint32_t it = 0, slot = 0;
         bool ok = true;
         for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
             const uint32_t rw = (tile % p.row_tiles) * 256 + 128 * rank + 32 * q;      // the warp's first row
             const uint32_t cb = tile / p.row_tiles;
-            const uint32_t r = rw + lane, rc = min(r, p.R - 1);
+            const uint32_t r = rw + lane;
             const uint32_t n0 = cb * (OP == kFp8Gated ? 128 : 256);                    // the tile's first column
-            // scales of block t, read two blocks ahead: the row's, and the columns' (one per 128, or one per column)
-            const float* sap = p.sa + rc;
-            const float *sbp0 = p.sb, *sbp1 = p.sb;
-            const uint32_t sb_step = OP == kFp8Dgrad ? cblocks : 1;
-            if (OP == kFp8Gated) {
-                sbp0 = p.sb + (size_t)cb * blocks;
-                sbp1 = p.sb + (size_t)(cb + cblocks) * blocks;
-            } else if (!C::SB_COL) {
-                const uint32_t nb = min(n0 / 128 + g, cblocks - 1);
-                sbp0 = OP == kFp8Dgrad ? p.sb + nb : p.sb + (size_t)nb * blocks;
-            }
-            const auto row_scale = [&](uint32_t t) {
-                return t < blocks && in_bounds((uint64_t)t * p.R + rc, 1, sa_n, p.status) ? __ldg(sap + (size_t)t * p.R) : 0.0f;
-            };
-            const auto tile_scale = [&](const float* sb, uint32_t t) { return t < blocks ? __ldg(sb + (size_t)t * sb_step) : 0.0f; };
-            // wgrad: this lane's four of the warp's 128 column scales (C is a multiple of 16)
-            const uint32_t sc = n0 + 128 * g + 4 * lane;
-            const auto col_scales = [&](uint32_t t) {
-                if (t < blocks && sc < p.C && in_bounds((uint64_t)t * p.C + sc, 4, sbc_n, p.status))
-                    return __ldg(reinterpret_cast<const float4*>(p.sb + (size_t)t * p.C + sc));
-                return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            };
-            uint64_t acc[4][16] = {};
-            float sa_a = row_scale(0), sa_b = row_scale(1);
-            float b0_a = 0, b0_b = 0, b1_a = 0, b1_b = 0;
-            float4 bc_a, bc_b;
-            if (C::SB_COL) {
-                bc_a = col_scales(0);
-                bc_b = col_scales(1);
-            } else {
-                b0_a = tile_scale(sbp0, 0);
-                b0_b = tile_scale(sbp0, 1);
-                if (OP == kFp8Gated) {
-                    b1_a = tile_scale(sbp1, 0);
-                    b1_b = tile_scale(sbp1, 1);
-                }
-            }
+            uint64_t acc[32] = {};                          // columns 2i, 2i + 1 of the warp's 64
             for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                const uint32_t b = it & 1;
-                float f0 = sa_a, f1;
-                if (C::SB_COL) {
-                    *reinterpret_cast<float4*>(s_sb + 128 * b + 4 * lane) = bc_a;
-                    bc_a = bc_b;
-                    bc_b = col_scales(t + 2);
-                    __syncwarp();
-                    f1 = f0;
-                } else {
-                    f1 = OP == kFp8Gated ? __fmul_rn(sa_a, b1_a) : 0.0f;
-                    f0 = __fmul_rn(sa_a, b0_a);
-                    if (OP != kFp8Gated) f1 = f0;
-                    b0_a = b0_b;
-                    b0_b = tile_scale(sbp0, t + 2);
-                    if (OP == kFp8Gated) {
-                        b1_a = b1_b;
-                        b1_b = tile_scale(sbp1, t + 2);
-                    }
+                const uint32_t b = h + 2 * (it & 1);
+                if (!fp8_wait(sfull0 + 8 * (it % C::SLOTS), (it / C::SLOTS) & 1, abort_flag, p.wait_ns)) {
+                    ok = false;
+                    break;
                 }
-                sa_a = sa_b;
-                sa_b = row_scale(t + 2);
+                const float* scale = reinterpret_cast<const float*>(smem + C::OFF_SCALE + (it % C::SLOTS) * C::SLOT_BYTES);
+                const float sa = scale[32 * q + lane];
+                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, scale[128 + (OP == kFp8Gated ? 0 : j2)]);
+                const float f1 = OP == kFp8Gated ? __fmul_rn(sa, scale[129]) : f0;
                 const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
                 if (!fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const auto add = [&](const uint32_t (&v)[32], int j) {
+                const auto add = [&](const uint32_t (&v)[16], int j) {
                     const uint64_t s = j < 2 ? s0 : s1;
-                    const float4* sb = reinterpret_cast<const float4*>(s_sb + 128 * b + 32 * j);
+                    const float4* sb = reinterpret_cast<const float4*>(scale + 128 + tcol + 16 * j);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         uint64_t x = f32x2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
                         uint64_t y = f32x2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
                         if (C::SB_COL) {
@@ -401,17 +415,17 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                             x = f32x2_mul(x, f32x2_pack(c.x, c.y));
                             y = f32x2_mul(y, f32x2_pack(c.z, c.w));
                         }
-                        f32x2_fma(acc[j][2 * i], x, s);
-                        f32x2_fma(acc[j][2 * i + 1], y, s);
+                        f32x2_fma(acc[8 * j + 2 * i], x, s);
+                        f32x2_fma(acc[8 * j + 2 * i + 1], y, s);
                     }
                 };
                 // a chunk's load runs while the chunk before it is added
-                uint32_t v[2][32];
-                tc_ld_32x32b_x32(lanes + b * 256 + chunk_col(0), v[0]);
+                uint32_t v[2][16];
+                tc_ld_32x32b_x16(lanes + b * 128 + chunk_col(0), v[0]);
                 tc_wait_ld(v[0]);
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
-                    tc_ld_32x32b_x32(lanes + b * 256 + chunk_col(j + 1), v[(j + 1) & 1]);
+                    tc_ld_32x32b_x16(lanes + b * 128 + chunk_col(j + 1), v[(j + 1) & 1]);
                     add(v[j & 1], j);
                     tc_wait_ld(v[(j + 1) & 1]);
                 }
@@ -426,55 +440,57 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 const uint64_t h_n = (uint64_t)p.R * p.C;
                 if (p.save && rw < p.R) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         uint32_t o[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 x = f32x2_unpack(acc[j][i]);
+                            const float2 x = f32x2_unpack(acc[16 * j + i]);
                             o[i] = bf16x2_of(x.x, x.y);
                         }
-                        fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)(n0 + (j >> 1) * p.C + 64 * g + 32 * (j & 1)),
-                                        (int32_t)rw, lane, false);
+                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)(n0 + j * p.C + tcol), (int32_t)rw, lane, false);
                     }
                 }
-                float h[64];
+                float y[32];
                 uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float2 x = f32x2_unpack(acc[i >> 4][i & 15]), u = f32x2_unpack(acc[2 + (i >> 4)][i & 15]);
-                    h[2 * i] = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
-                    h[2 * i + 1] = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
-                    m = max(m, max(abs_bits(h[2 * i]), abs_bits(h[2 * i + 1])));
+                for (int i = 0; i < 16; ++i) {
+                    const float2 x = f32x2_unpack(acc[i]), u = f32x2_unpack(acc[16 + i]);
+                    y[2 * i] = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
+                    y[2 * i + 1] = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
+                    m = max(m, max(abs_bits(y[2 * i]), abs_bits(y[2 * i + 1])));
                 }
-                // the block of 128 columns is shared by the two warps of this lane quarter
-                uint32_t* am = s_amax + (32 * q + lane) * 2;
-                am[g] = m;
-                named_barrier_sync(1 + q, 64);
-                m = max(m, am[g ^ 1]);
-                named_barrier_sync(1 + q, 64);           // read before the next tile's is written
+                // The row's block of 128 columns is shared by the four warps of this lane quarter.  Three
+                // slots in turn: the one zeroed here was last read before the previous tile's barrier
+                // and is first written after this one's.
+                uint32_t* am = s_amax + 32 * q + lane;
+                if (h + j2 == 0) am[128 * ((slot + 1) % 3)] = 0;
+                atomicMax(am + 128 * slot, m);
+                named_barrier_sync(1 + q, 128);
+                m = am[128 * slot];
+                slot = (slot + 1) % 3;
                 if (r < p.R) {
                     const Fp8Scale s = fp8_block_scale(m, p.status);
-                    const uint64_t at = (uint64_t)r * p.C + n0 + 64 * g;
-                    if (in_bounds(at, 64, h_n, p.status)) {
+                    const uint64_t at = (uint64_t)r * p.C + n0 + tcol;
+                    if (in_bounds(at, 32, h_n, p.status)) {
                         uint4* d = reinterpret_cast<uint4*>(p.h_codes + at);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float* x = h + 16 * i + 4 * e;
+                                const float* x = y + 16 * i + 4 * e;
                                 w[e] = cvt_e4m3x4(x[0] * s.factor, x[1] * s.factor, x[2] * s.factor, x[3] * s.factor);
                             }
                             d[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (g == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
+                    if (h + j2 == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
                         p.h_scales[(size_t)cb * p.R + r] = s.scale;
                 }
             } else if (rw < p.R) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t c = n0 + 128 * g + 32 * j;
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t c = n0 + tcol + 32 * j;
                     if (c >= p.C) continue;
                     uint32_t o[16];
                     if (OP == kFp8Wgrad) {
@@ -482,18 +498,18 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                         for (int part = 0; part < 2; ++part) {          // 16 FP32 columns a chunk
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float2 x = f32x2_unpack(acc[j][8 * part + i]);
+                                const float2 x = f32x2_unpack(acc[16 * j + 8 * part + i]);
                                 o[2 * i] = __float_as_uint(x.x);
                                 o[2 * i + 1] = __float_as_uint(x.y);
                             }
                             if (c + 16 * part < p.C)
-                                fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)(c + 16 * part), (int32_t)rw, lane,
+                                fp8_store_chunk(o, staging, &tmap_out, (int32_t)(c + 16 * part), (int32_t)rw, lane,
                                                 p.accumulate);
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float2 x = f32x2_unpack(acc[j][i]);
+                            float2 x = f32x2_unpack(acc[16 * j + i]);
                             // C is a multiple of 8, so a pair of columns is inside or outside
                             if (OP == kFp8Linear && p.bias && c + 2 * i < p.C) {
                                 const __nv_bfloat162 bb = *reinterpret_cast<const __nv_bfloat162*>(p.bias + c + 2 * i);
@@ -502,7 +518,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                             }
                             o[i] = bf16x2_of(x.x, x.y);
                         }
-                        fp8_store_chunk<C::CHUNK_BUFS>(o, staging, chunk, &tmap_out, (int32_t)c, (int32_t)rw, lane, false);
+                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)c, (int32_t)rw, lane, false);
                     }
                 }
             }
