@@ -10,7 +10,7 @@
 //
 // The scales are FP32, so the tensor core cannot apply them (its own block
 // scales are powers of two): each block's sum is taken by MMAs into tensor
-// memory, and 16 epilogue warps read it, multiply by the scales and add it to
+// memory, and 8 epilogue warps read it, multiply by the scales and add it to
 // the FP32 total in their registers while the MMAs go on.
 //
 // CTA pairs, one per two SMs, persistent over 256 x 256 output tiles (gated: 256
@@ -29,13 +29,17 @@
 // three hand-overs between threads (about 300 cycles each) and the drain; with
 // two 256-wide accumulators the tensor pipe stood idle for half of that time
 // (4608 x 12288 x 4096: 242 us against LATER us with units).
-// Warps 0-15: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31,
-// columns 64 (w / 8) .. + 63 of unit (w / 4) % 2 (gated: 32 of gate and of up);
-// 16: tile loads; 17 and 18: MMAs (in the leader CTA) of unit 0 and of unit 1:
-// the tensor pipe queues little, and while one warp goes through its barriers
-// the other's MMAs run; 19: scales, into a ring of eight blocks.  They are loaded
-// as far ahead as the tiles: L2 answers after some 2,000 cycles while the tiles
-// stream in, and reading them two blocks ahead in the epilogue cost 80 us of 298.
+// Warps 0-7: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of
+// units h = w / 4; 8: tile loads; 9: scales, by 4-byte copies into a ring of eight
+// blocks, as far ahead as the tiles (L2 answers after some 2,000 cycles while the
+// tiles stream in: reading them two blocks ahead in the epilogue cost 80 us of
+// 298); 10-13: MMAs (in the leader CTA), a warp per accumulator.  One thread spends
+// at least 86 cycles on issuing an MMA that takes the tensor pipe 64, and 130 on a
+// commit: four MMAs and two commits alone measured 390 cycles a unit from two
+// warps, 276 from four, where the pipe needs 256.
+// The totals take 128 registers of an epilogue thread; a spill in its loop goes
+// through a first-level cache that shared memory has left almost nothing of, and
+// cost a third of the kernel's time, hence the register split.
 // Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
 #pragma once
 #include <cstdint>
@@ -70,21 +74,24 @@ struct Fp8PairCfg {
     static constexpr bool A_MN = OP == kFp8Wgrad;                       // A's contiguous axis is its row axis
     static constexpr bool B_MN = OP == kFp8Wgrad || OP == kFp8Dgrad;
     static constexpr bool SB_COL = OP == kFp8Wgrad;                     // one B scale per column
-    static constexpr int EPI_WARPS = 16;
-    static constexpr int LOAD_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1, SCALE_WARP = EPI_WARPS + 3;
-    static constexpr int THREADS = 32 * (EPI_WARPS + 4);                // five warpgroups
-    // registers a thread: 640 x 96 at launch, shared out 512 x 112 + 128 x 32
-    static constexpr int EPI_REGS = 112, OTHER_REGS = 32;
-    static_assert(32 * EPI_WARPS * EPI_REGS + 128 * OTHER_REGS <= THREADS * 96, "register split");
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int LOAD_WARP = EPI_WARPS, SCALE_WARP = LOAD_WARP + 1, MMA_WARP = LOAD_WARP + 2, MMA_WARPS = 4;
+    static constexpr int THREADS = 32 * (EPI_WARPS + 8);                // four warpgroups
+    // registers a thread: 512 x 128 at launch, shared out 256 x 208 + 256 x 48
+    static constexpr int EPI_REGS = 208, OTHER_REGS = 48;
+    static_assert(32 * EPI_WARPS * EPI_REGS + 256 * OTHER_REGS <= THREADS * 128, "register split");
     static constexpr int TILE_BYTES = 128 * 128;                        // 128 rows x 128 bytes
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;                  // A and B tile of one CTA
-    static constexpr int STAGES = 5;
+    static constexpr int STAGES = 6;
     static constexpr int STAGING = 32 * 64;                             // per epilogue warp: one chunk
-    // scale slot of a block: 128 row scales, then 256 column scales or the two tile scales
-    static constexpr int SLOTS = 8;
+    // scale slot of a block: 128 row scales, then 256 column scales or the two tile scales; slots are
+    // filled GROUP blocks at a time, with one barrier a group
     static constexpr int SLOT_BYTES = 512 + (SB_COL ? 1024 : 16);
-    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 3 * 128 * 4 : 0;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int GROUP = SB_COL ? 2 : 4;
+    static constexpr int GROUPS = SB_COL ? 5 : 4;
+    static constexpr int SLOTS = GROUP * GROUPS;
+    static constexpr int AMAX_BYTES = OP == kFp8Gated ? 2 * 256 * 4 : 0;
+    static constexpr int BAR_BYTES = 384;
     static constexpr int SMEM_LIMIT = 232448;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_AMAX = OFF_STAGING + EPI_WARPS * STAGING;
@@ -98,7 +105,7 @@ struct Fp8PairCfg {
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
     static constexpr uint32_t B_UNIT = B_MN ? 64 : 64 * 128;            // from unit 0's B to unit 1's
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
-    static_assert((2 * STAGES + 10 + SLOTS) * 8 + 16 <= BAR_BYTES, "barriers");
+    static_assert((2 * STAGES + 8 + MMA_WARPS + 2 * GROUPS) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
 // Bounded wait of the pipeline: gives up after limit_ns or when *abort is set.
@@ -181,14 +188,16 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     // empty[s]:  both units' MMAs of the stage completed (commits multicast to both CTAs)
     // tfull[b]:  accumulator b (of unit b % 2) holds a block's sums (both CTAs)
     // tempty[b]: both CTAs' epilogue warps have read accumulator b (leader's barrier)
-    // sfull[i]:  scale slot i holds a block's scales (each lane of the scale warp arrives)
+    // sfull[i]:  group i of scale slots is filled (each lane of the scale warp arrives)
+    // sempty[i]: this CTA's epilogue warps are past group i
     const uint32_t full0 = smem_u32(bars);
     const uint32_t empty0 = full0 + 8 * C::STAGES;
     const uint32_t tfull0 = empty0 + 8 * C::STAGES;
     const uint32_t tempty0 = tfull0 + 32;
     const uint32_t drain0 = tempty0 + 32;
-    const uint32_t sfull0 = drain0 + 16;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 10 + C::SLOTS);
+    const uint32_t sfull0 = drain0 + 8 * C::MMA_WARPS;
+    const uint32_t sempty0 = sfull0 + 8 * C::GROUPS;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 8 + C::MMA_WARPS + 2 * C::GROUPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* never = abort_flag + 1;
 
@@ -202,11 +211,13 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         }
         for (int b = 0; b < 4; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, C::EPI_WARPS);      // half of each CTA's epilogue warps
+            mbar_init(tempty0 + 8 * b, 8);                 // four epilogue warps of each CTA
         }
-        mbar_init(drain0, 1);
-        mbar_init(drain0 + 8, 1);
-        for (int i = 0; i < C::SLOTS; ++i) mbar_init(sfull0 + 8 * i, 32);
+        for (int m = 0; m < C::MMA_WARPS; ++m) mbar_init(drain0 + 8 * m, 1);
+        for (int i = 0; i < C::GROUPS; ++i) {
+            mbar_init(sfull0 + 8 * i, 32);
+            mbar_init(sempty0 + 8 * i, C::EPI_WARPS);
+        }
         *abort_flag = 0;
         *never = 0;
         fence_mbarrier_init();
@@ -238,115 +249,87 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         if (warp == C::LOAD_WARP) {
             // ---------------------------------------------------------- tile loads (both CTAs)
             if (PLAIN_A || lane == 0) {
-                uint32_t it = 0;
-                bool ok = true;
-                // the plain copies of iteration j are complete: publish them to the leader's MMAs
-                const auto publish = [&](uint32_t j) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
-                };
-                for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
-                    const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
-                    const uint32_t cb = tile / p.row_tiles;
-                    const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
-                    for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                        const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                        if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-                        const int32_t k0 = (int32_t)(t * 128);
-                        if (lane == 0) {
-                            const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
-                            if (rank == 0)
-                                mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
-                            if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
-                            tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
-                        }
-                        if (PLAIN_A) {
-                            if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
-                            else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
-                            cp_async_commit();
-                            if (it > 0) {
-                                cp_async_wait<1>();
-                                publish(it - 1);
-                            }
-                        }
-                    }
-                }
-                if (PLAIN_A && it > 0) {
-                    cp_async_wait<0>();
-                    publish(it - 1);
-                }
-                if (lane == 0) {
-                    if (!ok) gave_up();
-                    // Neither CTA leaves while a load it issued may be in flight: the leader's
-                    // barriers count both CTAs' bytes; the peer learns of its own through the
-                    // commits of the MMAs that consumed them.
-                    for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                        fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never, kFp8WaitNs);
-                }
-            }
-        } else if (warp == C::MMA_WARP || warp == C::MMA_WARP + 1) {
-            // ---------------------------------------------------------- MMAs (leader), one warp per unit
-            if (lane == 0 && rank == 0) {
-                const uint32_t h = warp - C::MMA_WARP;
-                const uint32_t my_tiles = num_tiles > pair ? (num_tiles - pair + npairs - 1) / npairs : 0;
-                const uint32_t total = my_tiles * blocks;
-                bool ok = true;
-                for (uint32_t it = 0; it < total; ++it) {
-                    const uint32_t s = it % C::STAGES, b = h + 2 * (it & 1), use = it >> 1;
-                    if (!fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns) ||
-                        (use > 0 && !fp8_wait(tempty0 + 8 * b, (use - 1) & 1, abort_flag, p.wait_ns))) {
+            uint32_t it = 0;
+            bool ok = true;
+            // the plain copies of iteration j are complete: publish them to the leader's MMAs
+            const auto publish = [&](uint32_t j) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
+            };
+            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const uint32_t cb = tile / p.row_tiles;
+                const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
+                const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
+                for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-#pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        tc_mma_f8_pair(tmem + b * 128, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
-                                       smem_desc(st + C::TILE_BYTES + h * C::B_UNIT + k * C::B_STEP, 1024, 1024, 2), C::IDESC,
-                                       k != 0);
-                    tc_commit_pair_mc(tfull0 + 8 * b, 0x3);
-                    tc_commit_pair_mc(empty0 + 8 * s, 0x3);
+                    const int32_t k0 = (int32_t)(t * 128);
+                    if (lane == 0) {
+                        const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
+                        if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
+                        tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
+                    }
+                    if (PLAIN_A) {
+                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
+                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
+                        cp_async_commit();
+                        if (it > 0) {
+                            cp_async_wait<1>();
+                            publish(it - 1);
+                        }
+                    }
                 }
+            }
+            if (PLAIN_A && it > 0) {
+                cp_async_wait<0>();
+                publish(it - 1);
+            }
+            if (lane == 0) {
                 if (!ok) gave_up();
-                tc_commit_pair(drain0 + 8 * h);
-                fp8_wait(drain0 + 8 * h, 0, never, kFp8WaitNs);
+                // Neither CTA leaves while a load it issued may be in flight: the leader's
+                // barriers count both CTAs' bytes; the peer learns of its own through the
+                // commits of the MMAs that consumed them.
+                for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                    fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never, kFp8WaitNs);
+            }
             }
         } else if (warp == C::SCALE_WARP) {
             // ---------------------------------------------------------- scales (both CTAs)
-            // Slot it % 8 held block it - 8.  The MMAs of block it - STAGES (whose completion is
-            // waited for) overwrote the accumulators of block it - STAGES - 2, so every epilogue warp
-            // had released those and, in order, was past block it - 8.
-            static_assert(C::STAGES + 2 <= C::SLOTS, "scale ring");
             const uint32_t cblocks = (p.C + 127) / 128;
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
-                const uint32_t r0 = (tile % p.row_tiles) * 256 + 128 * rank + lane, cb = tile / p.row_tiles;
+                const uint32_t r0 = (tile % p.row_tiles) * 256 + 128 * rank, cb = tile / p.row_tiles;
                 const uint32_t nb = OP == kFp8Gated ? cb + (lane & 1) * cblocks : min(2 * cb + (lane & 1), cblocks - 1);
                 for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                    if (it >= (uint32_t)C::STAGES &&
-                        !fp8_wait(empty0 + 8 * (it % C::STAGES), (it / C::STAGES - 1) & 1, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
+                    if (it % C::GROUP == 0) {
+                        const uint32_t n = it / C::GROUP;
+                        if (n > 0) cp_async_arrive(sfull0 + 8 * ((n - 1) % C::GROUPS));
+                        if (n >= (uint32_t)C::GROUPS &&
+                            !fp8_wait(sempty0 + 8 * (n % C::GROUPS), (n / C::GROUPS - 1) & 1, abort_flag, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
                     }
                     const uint32_t slot = smem_u32(smem + C::OFF_SCALE + (it % C::SLOTS) * C::SLOT_BYTES);
                     const float* sa = p.sa + (size_t)t * p.R;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t r = r0 + 32 * i;
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        const uint32_t r = r0 + lane + 32 * i;
                         const bool in = r < p.R && in_bounds((uint64_t)t * p.R + r, 1, (uint64_t)blocks * p.R, p.status);
                         cp_async4_zfill(slot + 4 * (lane + 32 * i), in ? sa + r : p.sa, in ? 4 : 0);
                     }
                     if (C::SB_COL) {
                         const float* sb = p.sb + (size_t)t * p.C;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {           // C is a multiple of 16
+                        for (uint32_t i = 0; i < 2; ++i) {              // C is a multiple of 16
                             const uint32_t c = cb * 256 + 4 * (lane + 32 * i);
                             const bool in = c < p.C && in_bounds((uint64_t)t * p.C + c, 4, (uint64_t)blocks * p.C, p.status);
                             cp_async16_zfill(slot + 512 + 16 * (lane + 32 * i), in ? sb + c : p.sb, in ? 16 : 0);
@@ -356,56 +339,85 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                         const bool in = in_bounds(at, 1, (uint64_t)blocks * (OP == kFp8Gated ? 2 : 1) * cblocks, p.status);
                         cp_async4_zfill(slot + 512 + 4 * lane, in ? p.sb + at : p.sb, in ? 4 : 0);
                     }
-                    cp_async_arrive(sfull0 + 8 * (it % C::SLOTS));
                 }
             }
+            if (it > 0) cp_async_arrive(sfull0 + 8 * ((it - 1) / C::GROUP % C::GROUPS));   // the last group, whole or not
             if (!ok && lane == 0) gave_up();
             cp_async_commit();
             cp_async_wait<0>();
+        } else if (warp < C::MMA_WARP + C::MMA_WARPS) {
+            // ---------------------------------------------------------- MMAs (leader), a warp per accumulator
+            // Warp m fills accumulator m: unit m % 2 of every other block, and so of every other stage.
+            static_assert(C::STAGES % 2 == 0 && C::MMA_WARPS == 4, "a warp sees every phase of its stages' barriers");
+            if (lane == 0 && rank == 0) {
+                const uint32_t m = warp - C::MMA_WARP;
+                const uint32_t my_tiles = num_tiles > pair ? (num_tiles - pair + npairs - 1) / npairs : 0;
+                const uint32_t total = my_tiles * blocks;
+                bool ok = true;
+                for (uint32_t it = m >> 1; it < total; it += 2) {
+                    const uint32_t s = it % C::STAGES;
+                    if (!fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns) ||
+                        (it >= 2 && !fp8_wait(tempty0 + 8 * m, ((it >> 1) - 1) & 1, abort_flag, p.wait_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES), bt = st + C::TILE_BYTES + (m & 1) * C::B_UNIT;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        tc_mma_f8_pair(tmem + m * 128, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
+                                       smem_desc(bt + k * C::B_STEP, 1024, 1024, 2), C::IDESC, k != 0);
+                    tc_commit_pair_mc(tfull0 + 8 * m, 0x3);
+                    tc_commit_pair_mc(empty0 + 8 * s, 0x3);
+                }
+                if (!ok) gave_up();
+                tc_commit_pair(drain0 + 8 * m);
+                fp8_wait(drain0 + 8 * m, 0, never, kFp8WaitNs);
+            }
         }
     } else {
         regs_inc<C::EPI_REGS>();
         // ---------------------------------------------------------- epilogue (both CTAs)
-        const uint32_t q = warp & 3, h = (warp >> 2) & 1, j2 = warp >> 3;
+        const uint32_t q = warp & 3, h = warp >> 2;
         uint8_t* staging = smem + C::OFF_STAGING + warp * C::STAGING;
         uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
-        if (OP == kFp8Gated) {
-            if (threadIdx.x < 384) s_amax[threadIdx.x] = 0;
-            named_barrier_sync(5, 32 * C::EPI_WARPS);
-        }
-        // the warp's 64 columns of the tile (gated: 32 of gate, and the same of up)
-        const uint32_t tcol = OP == kFp8Gated ? 64 * h + 32 * j2 : 128 * j2 + 64 * h;
-        // chunk j (16 columns) in the unit's accumulator
-        const auto chunk_col = [&](uint32_t j) { return OP == kFp8Gated ? 32 * j2 + 16 * (j & 1) + 64 * (j >> 1) : 64 * j2 + 16 * j; };
+        // column i of a unit (i < 64: of the first 128 of the tile, gated: of gate) is tile column
+        // 64 h + i, or 64 h + 64 + i
         const uint32_t lanes = tmem + ((32 * q) << 16);
         const uint32_t cblocks = (p.C + 127) / 128;
-        uint32_t it = 0, slot = 0;
-        bool ok = true;
+        // where this CTA's releases go: the leader's barriers
+        const uint32_t release0 = mapa_shared(tempty0 + 8 * h, 0), release1 = mapa_shared(tempty0 + 8 * (h + 2), 0);
+        uint32_t it = 0, slot = 0, sslot = 0, sphase = 0;
+        bool ok = true, ready = false;
         for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
             const uint32_t rw = (tile % p.row_tiles) * 256 + 128 * rank + 32 * q;      // the warp's first row
             const uint32_t cb = tile / p.row_tiles;
             const uint32_t r = rw + lane;
             const uint32_t n0 = cb * (OP == kFp8Gated ? 128 : 256);                    // the tile's first column
-            uint64_t acc[32] = {};                          // columns 2i, 2i + 1 of the warp's 64
+            uint64_t acc[64] = {};                          // columns 2i, 2i + 1 of the unit
             for (uint32_t t = 0; t < blocks; ++t, ++it) {
                 const uint32_t b = h + 2 * (it & 1);
-                if (!fp8_wait(sfull0 + 8 * (it % C::SLOTS), (it / C::SLOTS) & 1, abort_flag, p.wait_ns)) {
+                if (sslot % C::GROUP == 0 && !fp8_wait(sfull0 + 8 * (sslot / C::GROUP), sphase, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
-                const float* scale = reinterpret_cast<const float*>(smem + C::OFF_SCALE + (it % C::SLOTS) * C::SLOT_BYTES);
+                const float* scale = reinterpret_cast<const float*>(smem + C::OFF_SCALE + sslot * C::SLOT_BYTES);
+                if (++sslot == (uint32_t)C::SLOTS) {
+                    sslot = 0;
+                    sphase ^= 1;
+                }
                 const float sa = scale[32 * q + lane];
-                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, scale[128 + (OP == kFp8Gated ? 0 : j2)]);
-                const float f1 = OP == kFp8Gated ? __fmul_rn(sa, scale[129]) : f0;
+                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, scale[128]);
+                const float f1 = C::SB_COL ? sa : __fmul_rn(sa, scale[129]);
                 const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
-                if (!fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
+                if (!ready && !fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const auto add = [&](const uint32_t (&v)[16], int j) {
-                    const uint64_t s = j < 2 ? s0 : s1;
-                    const float4* sb = reinterpret_cast<const float4*>(scale + 128 + tcol + 16 * j);
+                    const uint64_t s = j < 4 ? s0 : s1;
+                    const float4* sb = reinterpret_cast<const float4*>(scale + 128 + 64 * h + 16 * j + (j < 4 ? 0 : 64));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint64_t x = f32x2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
@@ -420,77 +432,82 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     }
                 };
                 // a chunk's load runs while the chunk before it is added
+                const uint32_t src = lanes + b * 128;
                 uint32_t v[2][16];
-                tc_ld_32x32b_x16(lanes + b * 128 + chunk_col(0), v[0]);
+                tc_ld_32x32b_x16(src, v[0]);
                 tc_wait_ld(v[0]);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    tc_ld_32x32b_x16(lanes + b * 128 + chunk_col(j + 1), v[(j + 1) & 1]);
+                for (int j = 0; j < 7; ++j) {
+                    tc_ld_32x32b_x16(src + 16 * (j + 1), v[(j + 1) & 1]);
                     add(v[j & 1], j);
                     tc_wait_ld(v[(j + 1) & 1]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 // the loads have returned, and the signal publishes no memory writes
-                if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(tempty0 + 8 * b, 0));
-                add(v[1], 3);
+                if (lane == 0) mbar_arrive_relaxed_cluster(b == h ? release0 : release1);
+                // look at the next block's accumulator while the last chunk is added
+                ready = mbar_test(tfull0 + 8 * (b ^ 2), ((it + 1) >> 1) & 1);
+                add(v[1], 7);
+                if (sslot % C::GROUP == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty0 + 8 * ((sslot == 0 ? C::GROUPS : sslot / C::GROUP) - 1));
+                }
             }
             if (!ok) break;
             if (OP == kFp8Gated) {
                 const uint64_t h_n = (uint64_t)p.R * p.C;
                 if (p.save && rw < p.R) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         uint32_t o[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float2 x = f32x2_unpack(acc[16 * j + i]);
                             o[i] = bf16x2_of(x.x, x.y);
                         }
-                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)(n0 + j * p.C + tcol), (int32_t)rw, lane, false);
+                        fp8_store_chunk(o, staging, &tmap_out, (int32_t)(n0 + (j >> 1) * p.C + 64 * h + 32 * (j & 1)), (int32_t)rw,
+                                        lane, false);
                     }
                 }
-                float y[32];
                 uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 x = f32x2_unpack(acc[i]), u = f32x2_unpack(acc[16 + i]);
-                    y[2 * i] = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
-                    y[2 * i + 1] = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
-                    m = max(m, max(abs_bits(y[2 * i]), abs_bits(y[2 * i + 1])));
+                for (int i = 0; i < 32; ++i) {             // acc[i] becomes H
+                    const float2 x = f32x2_unpack(acc[i]), u = f32x2_unpack(acc[32 + i]);
+                    const float y0 = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
+                    const float y1 = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
+                    m = max(m, max(abs_bits(y0), abs_bits(y1)));
+                    acc[i] = f32x2_pack(y0, y1);
                 }
-                // The row's block of 128 columns is shared by the four warps of this lane quarter.  Three
-                // slots in turn: the one zeroed here was last read before the previous tile's barrier
-                // and is first written after this one's.
-                uint32_t* am = s_amax + 32 * q + lane;
-                if (h + j2 == 0) am[128 * ((slot + 1) % 3)] = 0;
-                atomicMax(am + 128 * slot, m);
-                named_barrier_sync(1 + q, 128);
-                m = am[128 * slot];
-                slot = (slot + 1) % 3;
+                // The row's block of 128 columns is shared by the two warps of this lane quarter.
+                uint32_t* am = s_amax + 256 * slot + 32 * q + lane;
+                am[128 * h] = m;
+                named_barrier_sync(1 + q, 64);
+                m = max(m, am[128 * (h ^ 1)]);
+                slot ^= 1;                                 // the next tile's writes may pass this one's reads
                 if (r < p.R) {
                     const Fp8Scale s = fp8_block_scale(m, p.status);
-                    const uint64_t at = (uint64_t)r * p.C + n0 + tcol;
-                    if (in_bounds(at, 32, h_n, p.status)) {
+                    const uint64_t at = (uint64_t)r * p.C + n0 + 64 * h;
+                    if (in_bounds(at, 64, h_n, p.status)) {
                         uint4* d = reinterpret_cast<uint4*>(p.h_codes + at);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float* x = y + 16 * i + 4 * e;
-                                w[e] = cvt_e4m3x4(x[0] * s.factor, x[1] * s.factor, x[2] * s.factor, x[3] * s.factor);
+                                const float2 x = f32x2_unpack(acc[8 * i + 2 * e]), y = f32x2_unpack(acc[8 * i + 2 * e + 1]);
+                                w[e] = cvt_e4m3x4(x.x * s.factor, x.y * s.factor, y.x * s.factor, y.y * s.factor);
                             }
                             d[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (h + j2 == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
+                    if (h == 0 && in_bounds((uint64_t)cb * p.R + r, 1, (uint64_t)cblocks * p.R, p.status))
                         p.h_scales[(size_t)cb * p.R + r] = s.scale;
                 }
             } else if (rw < p.R) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t c = n0 + tcol + 32 * j;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t c = n0 + 128 * (j >> 1) + 64 * h + 32 * (j & 1);
                     if (c >= p.C) continue;
                     uint32_t o[16];
                     if (OP == kFp8Wgrad) {
