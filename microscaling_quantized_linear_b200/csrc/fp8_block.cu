@@ -9,6 +9,7 @@
 #include "fp8_gated.cuh"
 #include "fp8_gemm.cuh"
 #include "fp8_quantize.cuh"
+#include "fp8_short.cuh"
 #include "host.h"
 #include "nvq.h"
 
@@ -59,10 +60,10 @@ int launch(void (*kernel)(KArgs...), uint32_t grid, uint32_t block, size_t smem,
 
 // A dense [rows, cols] code matrix in tiles of 128 rows x 128 bytes, swizzled as
 // the MMA reads them; what lies outside reads as zeros.
-int codes_map(HostEncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t cols) {
+int codes_map(HostEncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t cols, uint32_t box_rows = 128) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols};
-    const cuuint32_t box[2] = {128u, 128u}, estr[2] = {1u, 1u};
+    const cuuint32_t box[2] = {128u, box_rows}, estr[2] = {1u, 1u};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? NVQ_OK : NVQ_ERR_CUDA;
@@ -84,6 +85,18 @@ struct Fp8Gemm {
     int64_t ldo;
     Fp8GemmParams p;
 };
+
+// Raise a kernel's shared-memory limit, once per device (`opted`: bit per device).
+template <typename Kernel>
+int opt_in(Kernel kern, int bytes, int device, std::atomic<uint64_t>& opted) {
+    if (opted.load(std::memory_order_acquire) >> device & 1) return NVQ_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return NVQ_ERR_CUDA;
+    }
+    opted.fetch_or(uint64_t(1) << device, std::memory_order_release);
+    return NVQ_OK;
+}
 
 Fp8GemmParams gemm_params(const float* sa, const float* sb, int64_t R, int64_t C, int64_t T) {
     Fp8GemmParams p = {};
@@ -110,14 +123,8 @@ int launch_pair(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
     if (!g.out) mo = mb;                                 // not written
     else if ((rc = out_map(encode, &mo, g.out, OP == kFp8Wgrad, p.R, brows, g.ldo))) return rc;
     auto kern = fp8_gemm_pair_kernel<OP, PLAIN_A>;
-    static std::atomic<uint64_t> opted{0};               // devices whose shared-memory limit is raised
-    if (!(opted.load(std::memory_order_acquire) >> d.index & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess) {
-            cudaGetLastError();
-            return NVQ_ERR_CUDA;
-        }
-        opted.fetch_or(uint64_t(1) << d.index, std::memory_order_release);
-    }
+    static std::atomic<uint64_t> opted{0};
+    if ((rc = opt_in(kern, C::SMEM_BYTES, d.index, opted))) return rc;
     p.a = g.a;
     p.status = d.status;
     p.wait_ns = (uint32_t)host_wait_ns(kFp8WaitNs);
@@ -128,8 +135,58 @@ int launch_pair(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
     return launch(kern, 2 * (tiles < pairs ? tiles : pairs), C::THREADS, C::SMEM_BYTES, stream, 2, ma, mb, mo, p);
 }
 
+// Few tokens: one cluster of `split` CTAs per 128 output columns and TN tokens.
+template <int OP, int TN>
+int launch_short(const HostDevice& d, const Fp8Gemm& g, uint32_t split, nvq_stream_t stream) {
+    using C = Fp8ShortCfg<OP, TN>;
+    const HostEncodeTiledFn encode = host_encoder();
+    if (!encode) return NVQ_ERR_CUDA;
+    const int64_t wrows = C::P * (int64_t)g.p.C;
+    CUtensorMap mw, ma;
+    int rc;
+    if ((rc = codes_map(encode, &mw, g.b, C::W_MN ? g.p.T : wrows, C::W_MN ? wrows : g.p.T))) return rc;
+    if ((rc = codes_map(encode, &ma, g.a, g.p.R, g.p.T, TN))) return rc;
+    auto kern = fp8_short_kernel<OP, TN>;
+    static std::atomic<uint64_t> opted{0};
+    if ((rc = opt_in(kern, C::SMEM_BYTES, d.index, opted))) return rc;
+    Fp8ShortParams p = {};
+    p.sa = g.p.sa;
+    p.sw = g.p.sb;
+    p.bias = g.p.bias;
+    p.out = static_cast<__nv_bfloat16*>(g.out);
+    p.h_codes = g.p.h_codes;
+    p.h_scales = g.p.h_scales;
+    p.status = d.status;
+    p.M = g.p.R;
+    p.C = g.p.C;
+    p.T = g.p.T;
+    p.ldo = (uint32_t)g.ldo;
+    p.split = split;
+    p.wait_ns = (uint32_t)host_wait_ns(kFp8WaitNs);
+    const uint32_t tiles = (uint32_t)(blocks_of(p.C) * ((p.M + TN - 1) / TN));
+    return launch(kern, tiles * split, C::THREADS, C::SMEM_BYTES, stream, split, mw, ma, p);
+}
+
+// The split of the contracted axis: the most CTAs that one wave of the device holds, at least two
+// blocks to a CTA, so that the weight streams through as many SMs as possible.
+uint32_t short_split(uint64_t tiles, uint64_t blocks, uint32_t num_sms) {
+    uint32_t split = 8;
+    while (split > 1 && (tiles * split > num_sms || blocks < 2 * split)) split /= 2;
+    return split;
+}
+
+constexpr uint32_t kShortTokens = 64;
+
 template <int OP>
 int launch_gemm(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
+    if constexpr (OP == kFp8Linear || OP == kFp8Gated) {
+        if (g.p.R <= kShortTokens) {
+            const uint32_t split = short_split(blocks_of(g.p.C), blocks_of(g.p.T), d.num_sms);
+            if (g.p.R <= 16) return launch_short<OP, 16>(d, g, split, stream);
+            if (g.p.R <= 32) return launch_short<OP, 32>(d, g, split, stream);
+            return launch_short<OP, 64>(d, g, split, stream);
+        }
+    }
     // dY's rows may be 8 bytes past a multiple of 16, which a tensor map cannot describe
     if constexpr (OP == kFp8Dgrad || OP == kFp8Wgrad)
         if ((OP == kFp8Wgrad ? g.p.R : g.p.T) % 16) return launch_pair<OP, true>(d, g, stream);

@@ -183,7 +183,7 @@ def product_bounds(A, B, T, exact):
 LINEAR = [(1, 8, 16), (1, 264, 128), (1, 4096, 1024), (2, 136, 144), (8, 520, 2048), (16, 256, 384), (17, 248, 400),
           (31, 1032, 656), (32, 128, 128), (33, 384, 272), (64, 264, 1040), (65, 264, 512), (127, 128, 112), (128, 256, 256),
           (129, 264, 384), (200, 1288, 528), (256, 256, 2048), (257, 520, 144), (513, 776, 640), (1000, 2056, 336),
-          (600, 8200, 2320)]                            # more tiles than CTA pairs, more blocks than any ring
+          (5, 9224, 20496), (40, 264, 8208), (600, 8200, 2320)]                            # more tiles than CTA pairs, more blocks than any ring
 
 
 @pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
@@ -282,7 +282,7 @@ def e4m3_step_bound(v, scales, kind):
 
 
 GATED = [(1, 128, 16), (1, 1408, 1024), (3, 256, 144), (16, 384, 528), (17, 128, 272), (32, 640, 2048), (33, 256, 400),
-         (64, 128, 128), (100, 384, 1040), (129, 256, 272), (300, 512, 784), (640, 1408, 400), (600, 4224, 2320)]
+         (64, 128, 128), (100, 384, 1040), (129, 256, 272), (300, 512, 784), (640, 1408, 400), (1, 12288, 272), (7, 640, 16400), (48, 256, 4112), (600, 4224, 2320)]
 
 
 def sigmoid_error(g):
