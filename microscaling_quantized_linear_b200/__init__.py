@@ -529,6 +529,8 @@ def _scales(t, name, shape):
 
 def _bf16(t, name, rows=None, cols=None):
     """A row-major BF16 matrix with unit column stride; a single row may have any pitch."""
+    if t.dtype is torch.bfloat16 and t.dim() == 2 and t.stride(1) == 1 and rows is None:
+        return t
     if t.dtype != torch.bfloat16:
         raise ValueError("%s: expected torch.bfloat16, got %s" % (name, t.dtype))
     if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)) or (t.shape[1] > 1 and t.stride(1) != 1):
@@ -542,50 +544,38 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
-class _Call:
-    """Runs one library call on the tensors' device and the given (or current)
-    stream.  Outputs are allocated inside, so that they belong to that stream;
-    tensors used on a stream other than the current one are recorded on it, so
-    that their memory is not handed out again while the call may still run."""
+_device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, **tensors):
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
+
+def _here(stream, names, first, *rest):
+    """The current raw stream, where the call can run as things stand (no stream
+    asked for, the tensors on the current device); None where it has to run
+    inside _elsewhere.  Every tensor has to be on one CUDA device."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("%s: expected a CUDA tensor" % names[0])
+    for i, t in enumerate(rest):
+        if t is not None and t.get_device() != dev:
             if not t.is_cuda:
-                raise ValueError("%s: expected a CUDA tensor" % name)
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("%s: on %s, the other tensors on %s" % (name, t.device, dev))
-        self.device = dev
-        self.tensors = tensors
-        self.stream = stream
-        self.guard = None
-        if stream is not None and stream.device != dev:
-            raise ValueError("stream: on %s, the tensors on %s" % (stream.device, dev))
+                raise ValueError("%s: expected a CUDA tensor" % names[i + 1])
+            raise ValueError("%s: on %s, %s on %s" % (names[i + 1], t.device, names[0], first.device))
+    return _raw_stream(dev) if stream is None and dev == _device_now() else None
 
-    def __enter__(self):
-        if self.stream is not None and self.stream != torch.cuda.current_stream(self.device):
-            self.guard = torch.cuda.stream(self.stream)         # also makes its device current
-            self.guard.__enter__()
-            for t in self.tensors.values():
-                if t is not None:
-                    t.record_stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        self.raw = torch._C._cuda_getCurrentRawStream(self.device.index)
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+def _elsewhere(stream, *tensors):
+    """Context with the tensors' device and the given stream current: outputs
+    allocated inside belong to that stream, and the tensors are recorded on it,
+    so that their memory is not handed out again while the call may still run."""
+    dev = tensors[0].device
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError("stream: on %s, the tensors on %s" % (stream.device, dev))
+    if stream != torch.cuda.current_stream(dev):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def fp8_block_quantize(x, codes=None, scales=None, stream=None):
@@ -598,13 +588,16 @@ def fp8_block_quantize(x, codes=None, scales=None, stream=None):
         _codes(codes, "codes", (M, K))
     if scales is not None:
         _scales(scales, "scales", ((K + 127) // 128, M))
-    with _Call(stream, x=x, codes=codes, scales=scales) as c:
-        if codes is None:
-            codes = c.empty((M, K), torch.uint8)
-        if scales is None:
-            scales = c.empty(((K + 127) // 128, M), torch.float32)
-        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), codes.data_ptr(), scales.data_ptr(), None, None,
-                                       c.raw), "fp8_block_quantize")
+    raw = _here(stream, ("x", "codes", "scales"), x, codes, scales)
+    if raw is None:
+        with _elsewhere(stream, x, codes, scales):
+            return fp8_block_quantize(x, codes, scales)
+    if codes is None:
+        codes = x.new_empty((M, K), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty(((K + 127) // 128, M), dtype=torch.float32)
+    _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), codes.data_ptr(), scales.data_ptr(), None, None,
+                                   raw), "fp8_block_quantize")
     return codes, scales
 
 
@@ -617,13 +610,16 @@ def fp8_block_quantize_columns(x, codes=None, scales=None, stream=None):
         _codes(codes, "codes", (M, K))
     if scales is not None:
         _scales(scales, "scales", ((M + 127) // 128, K))
-    with _Call(stream, x=x, codes=codes, scales=scales) as c:
-        if codes is None:
-            codes = c.empty((M, K), torch.uint8)
-        if scales is None:
-            scales = c.empty(((M + 127) // 128, K), torch.float32)
-        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), None, None, codes.data_ptr(), scales.data_ptr(),
-                                       c.raw), "fp8_block_quantize")
+    raw = _here(stream, ("x", "codes", "scales"), x, codes, scales)
+    if raw is None:
+        with _elsewhere(stream, x, codes, scales):
+            return fp8_block_quantize_columns(x, codes, scales)
+    if codes is None:
+        codes = x.new_empty((M, K), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty(((M + 127) // 128, K), dtype=torch.float32)
+    _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), None, None, codes.data_ptr(), scales.data_ptr(),
+                                   raw), "fp8_block_quantize")
     return codes, scales
 
 
@@ -632,12 +628,15 @@ def fp8_block_quantize_both(x, stream=None):
     (row codes, row scales, column codes, column scales)."""
     _bf16(x, "x")
     M, K = x.shape
-    with _Call(stream, x=x) as c:
-        rc, cc = c.empty((M, K), torch.uint8), c.empty((M, K), torch.uint8)
-        rs = c.empty(((K + 127) // 128, M), torch.float32)
-        cs = c.empty(((M + 127) // 128, K), torch.float32)
-        _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), rc.data_ptr(), rs.data_ptr(), cc.data_ptr(),
-                                       cs.data_ptr(), c.raw), "fp8_block_quantize")
+    raw = _here(stream, ("x",), x)
+    if raw is None:
+        with _elsewhere(stream, x):
+            return fp8_block_quantize_both(x)
+    rc, cc = x.new_empty((M, K), dtype=torch.uint8), x.new_empty((M, K), dtype=torch.uint8)
+    rs = x.new_empty(((K + 127) // 128, M), dtype=torch.float32)
+    cs = x.new_empty(((M + 127) // 128, K), dtype=torch.float32)
+    _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), rc.data_ptr(), rs.data_ptr(), cc.data_ptr(),
+                                   cs.data_ptr(), raw), "fp8_block_quantize")
     return rc, rs, cc, cs
 
 
@@ -651,13 +650,16 @@ def fp8_block_quantize_weight(w, codes=None, scales=None, stream=None):
         _codes(codes, "codes", (N, K))
     if scales is not None:
         _scales(scales, "scales", shape)
-    with _Call(stream, w=w, codes=codes, scales=scales) as c:
-        if codes is None:
-            codes = c.empty((N, K), torch.uint8)
-        if scales is None:
-            scales = c.empty(shape, torch.float32)
-        _check(_lib.fp8_block_quantize_weight(w.data_ptr(), N, K, _ld(w), codes.data_ptr(), scales.data_ptr(), c.raw),
-               "fp8_block_quantize_weight")
+    raw = _here(stream, ("w", "codes", "scales"), w, codes, scales)
+    if raw is None:
+        with _elsewhere(stream, w, codes, scales):
+            return fp8_block_quantize_weight(w, codes, scales)
+    if codes is None:
+        codes = w.new_empty((N, K), dtype=torch.uint8)
+    if scales is None:
+        scales = w.new_empty(shape, dtype=torch.float32)
+    _check(_lib.fp8_block_quantize_weight(w.data_ptr(), N, K, _ld(w), codes.data_ptr(), scales.data_ptr(), raw),
+           "fp8_block_quantize_weight")
     return codes, scales
 
 
@@ -682,12 +684,15 @@ def fp8_block_linear(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, 
         _buf(bias, torch.bfloat16, 2 * N, "bias")
     if out is not None:
         _bf16(out, "out", M, N)
-    with _Call(stream, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out) as c:
-        if out is None:
-            out = c.empty((M, N), torch.bfloat16)
-        _check(_lib.fp8_block_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                     None if bias is None else bias.data_ptr(), out.data_ptr(), _ld(out), M, N, K,
-                                     c.raw), "fp8_block_linear")
+    raw = _here(stream, ("a_codes", "a_scales", "w_codes", "w_scales", "bias", "out"), a_codes, a_scales, w_codes, w_scales, bias, out)
+    if raw is None:
+        with _elsewhere(stream, a_codes, a_scales, w_codes, w_scales, bias, out):
+            return fp8_block_linear(a_codes, a_scales, w_codes, w_scales, bias, out)
+    if out is None:
+        out = a_codes.new_empty((M, N), dtype=torch.bfloat16)
+    _check(_lib.fp8_block_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                 None if bias is None else bias.data_ptr(), out.data_ptr(), _ld(out), M, N, K,
+                                 raw), "fp8_block_linear")
     return out
 
 
@@ -699,12 +704,15 @@ def fp8_block_linear_dgrad(dy_codes, dy_scales, w_codes, w_scales, out=None, str
         raise ValueError("dy_codes has %d columns, w_codes %d rows" % (Nd, N))
     if out is not None:
         _bf16(out, "out", M, K)
-    with _Call(stream, dy_codes=dy_codes, dy_scales=dy_scales, w_codes=w_codes, w_scales=w_scales, out=out) as c:
-        if out is None:
-            out = c.empty((M, K), torch.bfloat16)
-        _check(_lib.fp8_block_linear_dgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), w_codes.data_ptr(),
-                                           w_scales.data_ptr(), out.data_ptr(), _ld(out), M, N, K, c.raw),
-               "fp8_block_linear_dgrad")
+    raw = _here(stream, ("dy_codes", "dy_scales", "w_codes", "w_scales", "out"), dy_codes, dy_scales, w_codes, w_scales, out)
+    if raw is None:
+        with _elsewhere(stream, dy_codes, dy_scales, w_codes, w_scales, out):
+            return fp8_block_linear_dgrad(dy_codes, dy_scales, w_codes, w_scales, out)
+    if out is None:
+        out = dy_codes.new_empty((M, K), dtype=torch.bfloat16)
+    _check(_lib.fp8_block_linear_dgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), w_codes.data_ptr(),
+                                       w_scales.data_ptr(), out.data_ptr(), _ld(out), M, N, K, raw),
+           "fp8_block_linear_dgrad")
     return out
 
 
@@ -725,12 +733,15 @@ def fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out=None, acc
             raise ValueError("accumulate needs out")
     else:
         _mat(out, torch.float32, N, K, "out")
-    with _Call(stream, dy_codes=dy_codes, dy_scales=dy_scales, x_codes=x_codes, x_scales=x_scales, out=out) as c:
-        if out is None:
-            out = c.empty((N, K), torch.float32)
-        _check(_lib.fp8_block_linear_wgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), x_codes.data_ptr(),
-                                           x_scales.data_ptr(), out.data_ptr(), _ld(out), int(bool(accumulate)), M, N,
-                                           K, c.raw), "fp8_block_linear_wgrad")
+    raw = _here(stream, ("dy_codes", "dy_scales", "x_codes", "x_scales", "out"), dy_codes, dy_scales, x_codes, x_scales, out)
+    if raw is None:
+        with _elsewhere(stream, dy_codes, dy_scales, x_codes, x_scales, out):
+            return fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out, accumulate)
+    if out is None:
+        out = dy_codes.new_empty((N, K), dtype=torch.float32)
+    _check(_lib.fp8_block_linear_wgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), x_codes.data_ptr(),
+                                       x_scales.data_ptr(), out.data_ptr(), _ld(out), int(bool(accumulate)), M, N,
+                                       K, raw), "fp8_block_linear_wgrad")
     return out
 
 
@@ -745,14 +756,17 @@ def fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save=False, str
     if N % 256:
         raise ValueError("w_codes: %d rows, expected gate and up of a multiple of 128 each" % N)
     F = N // 2
-    with _Call(stream, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales) as c:
-        codes = c.empty((M, F), torch.uint8)
-        scales = c.empty((F // 128, M), torch.float32)
-        gate_up = c.empty((M, N), torch.bfloat16) if save else None
-        _check(_lib.fp8_block_gated_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
-                                           w_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                           gate_up.data_ptr() if save else None, N, M, F, K, c.raw),
-               "fp8_block_gated_linear")
+    raw = _here(stream, ("a_codes", "a_scales", "w_codes", "w_scales"), a_codes, a_scales, w_codes, w_scales)
+    if raw is None:
+        with _elsewhere(stream, a_codes, a_scales, w_codes, w_scales):
+            return fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save)
+    codes = a_codes.new_empty((M, F), dtype=torch.uint8)
+    scales = a_codes.new_empty((F // 128, M), dtype=torch.float32)
+    gate_up = a_codes.new_empty((M, N), dtype=torch.bfloat16) if save else None
+    _check(_lib.fp8_block_gated_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
+                                       w_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                       gate_up.data_ptr() if save else None, N, M, F, K, raw),
+           "fp8_block_gated_linear")
     return codes, scales, gate_up
 
 
@@ -764,15 +778,18 @@ def fp8_block_gated_backward(dh, gate_up, stream=None):
     M, F = dh.shape
     _bf16(gate_up, "gate_up", M, 2 * F)
     MB = (M + 127) // 128
-    with _Call(stream, dh=dh, gate_up=gate_up) as c:
-        rc, cc = c.empty((2, M, 2 * F), torch.uint8).unbind(0)
-        rs = c.empty(((2 * F + 127) // 128, M), torch.float32)
-        cs = c.empty((MB, 2 * F), torch.float32)
-        hc = c.empty((M, F), torch.uint8)
-        hs = c.empty((MB, F), torch.float32)
-        _check(_lib.fp8_block_gated_backward(dh.data_ptr(), _ld(dh), gate_up.data_ptr(), _ld(gate_up), rc.data_ptr(),
-                                             rs.data_ptr(), cc.data_ptr(), cs.data_ptr(), hc.data_ptr(), hs.data_ptr(),
-                                             M, F, c.raw), "fp8_block_gated_backward")
+    raw = _here(stream, ("dh", "gate_up"), dh, gate_up)
+    if raw is None:
+        with _elsewhere(stream, dh, gate_up):
+            return fp8_block_gated_backward(dh, gate_up)
+    rc, cc = dh.new_empty((2, M, 2 * F), dtype=torch.uint8).unbind(0)
+    rs = dh.new_empty(((2 * F + 127) // 128, M), dtype=torch.float32)
+    cs = dh.new_empty((MB, 2 * F), dtype=torch.float32)
+    hc = dh.new_empty((M, F), dtype=torch.uint8)
+    hs = dh.new_empty((MB, F), dtype=torch.float32)
+    _check(_lib.fp8_block_gated_backward(dh.data_ptr(), _ld(dh), gate_up.data_ptr(), _ld(gate_up), rc.data_ptr(),
+                                         rs.data_ptr(), cc.data_ptr(), cs.data_ptr(), hc.data_ptr(), hs.data_ptr(),
+                                         M, F, raw), "fp8_block_gated_backward")
     return (rc, rs), (cc, cs), (hc, hs)
 
 

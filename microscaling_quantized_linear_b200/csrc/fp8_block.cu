@@ -326,7 +326,11 @@ int fp8_block_gated_backward(const void* dh, int64_t lddh, const void* gate_up, 
     const GatedBwdParams p = {static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gate_up), (uint32_t)M,
                               (uint32_t)F, (uint32_t)lddh, (uint32_t)ldgu, row_codes, row_scales, col_codes,
                               col_scales, h_codes, h_scales, d.status};
-    return launch(fp8_gated_backward_kernel, (uint32_t)(blocks_of(M) * (F / 128)), kGatedBwdThreads, 0, stream, 1, p);
+    static std::atomic<uint64_t> opted{0};
+    if (int rc = opt_in(fp8_gated_backward_kernel, kGatedBwdSmem, d.index, opted)) return rc;
+    const int64_t tiles = blocks_of(M) * (F / 128);
+    return launch(fp8_gated_backward_kernel, (uint32_t)(tiles < d.num_sms ? tiles : d.num_sms), kGatedBwdThreads,
+                  kGatedBwdSmem, stream, 1, p);
 }
 
 }  // extern "C"

@@ -17,6 +17,7 @@
 namespace nvq {
 
 constexpr int kGatedBwdThreads = 512;
+constexpr int kGatedBwdSmem = 2 * 3 * 4 * 512 * 16 + 16 * 3 * 128 * 4 + 3 * 128 * 4;
 
 struct GatedBwdParams {
     const uint16_t* dh;         // [rows, F], pitch ld_dh
@@ -31,147 +32,218 @@ struct GatedBwdParams {
     unsigned int* status;
 };
 
-// sigma(g) = 1 / (1 + e), e = exp(-g), within about two units: e = 2^hi (1 + lo ln 2)
-// with hi + lo = -g log2(e) carried in two floats, so that a large |g| costs no
-// precision.  e overflows to infinity for g < -88, which gives 0.
-struct Sigmoid {
-    float s, one_minus;         // sigma(g), 1 - sigma(g)
-};
+// sigma(g) and 1 - sigma(g) of two values.  exp(-g) = 2^i 2^f with i the integer
+// nearest to -g log2(e), which is carried in two floats so that a large |g| costs
+// no precision, and 2^f, |f| <= 1/2, by its Taylor series to the seventh power (the
+// next term is below 2^-27): 0.44 units rms against 0.67 for expf and 0.97 for one
+// ex2.approx.  The reciprocal is the approximate one and a Newton step.  g is taken
+// within +-87; below, sigma (less than 2^-125) is taken as 0.
+__device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& one_minus) {
+    const auto two = [](float v) { return f32x2_pack(v, v); };
+    const float2 gv = f32x2_unpack(g);
+    const uint64_t gc = f32x2_pack(fminf(fmaxf(gv.x, -87.0f), 87.0f), fminf(fmaxf(gv.y, -87.0f), 87.0f));
+    const uint64_t hi = f32x2_mul(gc, two(-1.4426950216f));
+    const uint64_t lo = f32x2_fma3(gc, two(-1.9259630e-8f), f32x2_fma3(gc, two(-1.4426950216f), f32x2_mul(hi, two(-1.0f))));
+    const uint64_t rounded = f32x2_add(hi, two(12582912.0f));       // 1.5 2^23: the integer lands in the low bits
+    const uint64_t f = f32x2_add(f32x2_fma3(f32x2_add(rounded, two(-12582912.0f)), two(-1.0f), hi), lo);
+    uint64_t p = two(1.5252733804e-5f);                             // (ln 2)^k / k!, k = 7 .. 0
+    p = f32x2_fma3(p, f, two(1.5403530394e-4f));
+    p = f32x2_fma3(p, f, two(1.3333558146e-3f));
+    p = f32x2_fma3(p, f, two(9.6181291076e-3f));
+    p = f32x2_fma3(p, f, two(5.5504108665e-2f));
+    p = f32x2_fma3(p, f, two(0.2402265070f));
+    p = f32x2_fma3(p, f, two(0.6931471806f));
+    p = f32x2_fma3(p, f, two(1.0f));
+    const float2 pv = f32x2_unpack(p), rv = f32x2_unpack(rounded);
+    const uint64_t e = f32x2_pack(__uint_as_float(__float_as_uint(pv.x) + (__float_as_uint(rv.x) << 23)),
+                                  __uint_as_float(__float_as_uint(pv.y) + (__float_as_uint(rv.y) << 23)));
+    const uint64_t d = f32x2_add(e, two(1.0f)), neg = f32x2_fma3(e, two(-1.0f), two(-1.0f));
+    const float2 dv = f32x2_unpack(d);
+    float rx, ry;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(dv.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(dv.y));
+    const uint64_t r = f32x2_pack(rx, ry);
+    const uint64_t s = f32x2_fma3(r, f32x2_fma3(neg, r, two(1.0f)), r);
+    one_minus = f32x2_mul(e, s);
+    const float2 sv = f32x2_unpack(s);
+    sigma = f32x2_pack(gv.x < -87.0f ? 0.0f : sv.x, gv.y < -87.0f ? 0.0f : sv.y);
+}
 
-__device__ __forceinline__ float exp_neg(float g) {
-    const float hi = __fmul_rn(g, -1.4426950216f);
-    const float lo = __fmaf_rn(g, -1.9259630e-8f, __fmaf_rn(g, -1.4426950216f, -hi));
-    float e;
+// sigma(g) of one value in fewer registers, for the products' epilogues: ex2.approx of
+// the same two-float argument (0.81 units rms against 0.63).
+__device__ __forceinline__ float sigmoid1(float g) {
+    const float gc = fminf(fmaxf(g, -87.0f), 87.0f);
+    const float hi = __fmul_rn(gc, -1.4426950216f);
+    const float lo = __fmaf_rn(gc, -1.9259630e-8f, __fmaf_rn(gc, -1.4426950216f, -hi));
+    float e, r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(hi));
-    return fabsf(hi) < 126.0f ? __fmaf_rn(e, __fmul_rn(lo, 0.6931471806f), e) : e;
-}
-
-// 1 / (1 + e) to about half a unit: the approximate reciprocal and one Newton step
-// (not where 1 + e nears the largest floats, whose reciprocal needs no more).
-__device__ __forceinline__ float sigmoid_of_exp(float e) {
-    const float d = __fadd_rn(1.0f, e);
-    float r;
+    const float d = __fadd_rn(1.0f, __fmaf_rn(e, __fmul_rn(lo, 0.6931471806f), e));
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
-    return e < 1e30f ? __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r) : r;
+    return g < -87.0f ? 0.0f : __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return sigmoid_of_exp(exp_neg(g)); }
-
-__device__ __forceinline__ Sigmoid sigmoid_both(float g) {
-    const float e = exp_neg(g), s = sigmoid_of_exp(e);
-    return {s, e > 1e30f ? 1.0f : __fmul_rn(e, s)};
-}
-
-__device__ __forceinline__ uint2 fp8_codes8(const float* v, const float (&f)[8]) {
-    return make_uint2(cvt_e4m3x4(v[0] * f[0], v[1] * f[1], v[2] * f[2], v[3] * f[3]),
-                      cvt_e4m3x4(v[4] * f[4], v[5] * f[5], v[6] * f[6], v[7] * f[7]));
-}
+// SiLU(g) * u; the argument's NaN comes through the product.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, u), sigmoid1(g)); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// One CTA = a tile of 128 rows x 128 of F.  Thread: rows g + 32 i (i < 4) x 8 columns.
-__global__ void __launch_bounds__(kGatedBwdThreads)
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float amax_nan(float m, float v) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(m), "f"(fabsf(v)));
+    return o;
+}
+
+// Eight values (four pairs) times factors -> eight codes.
+__device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64_t (&f)[4]) {
+    const float2 a = f32x2_unpack(f32x2_mul(v[0], f[0])), b = f32x2_unpack(f32x2_mul(v[1], f[1]));
+    const float2 c = f32x2_unpack(f32x2_mul(v[2], f[2])), d = f32x2_unpack(f32x2_mul(v[3], f[3]));
+    return make_uint2(cvt_e4m3x4(a.x, a.y, b.x, b.y), cvt_e4m3x4(c.x, c.y, d.x, d.y));
+}
+
+// Persistent, one CTA per SM, over tiles of 128 rows x 128 of F; thread: rows
+// g + 32 i (i < 4) x 8 columns, its 96 results in registers.  The next tile's
+// inputs come in meanwhile (16-byte copies, each thread its own, no barrier).  HBM
+// sets the pace, 11 bytes a value, if a value costs less than about 60
+// instructions: hence packed pairs throughout.
+__global__ void __launch_bounds__(kGatedBwdThreads, 1)
 fp8_gated_backward_kernel(const GatedBwdParams p) {
-    __shared__ uint32_t s_max[16][3][128];
-    __shared__ float s_factor[3][128];
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4* in = reinterpret_cast<uint4*>(smem);                     // [2][12][512]
+    float* s_max = reinterpret_cast<float*>(smem + 2 * 12 * 512 * 16);          // [16 warps][3][128]
+    float* s_factor = s_max + 16 * 3 * 128;                                     // [3][128]
     griddep_wait();
     griddep_launch();
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t h = lane & 15, g = threadIdx.x >> 4;
-    const uint32_t fblocks = p.F / 128;
-    const uint32_t fb = blockIdx.x % fblocks, rb = blockIdx.x / fblocks, r0 = rb * 128;
-    const uint32_t c = fb * 128 + h * 8;
-    const uint32_t F2 = 2 * p.F, mblocks = (p.rows + 127) / 128;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t h = lane & 15, g = tid >> 4;
+    const uint32_t fblocks = p.F / 128, mblocks = (p.rows + 127) / 128, tiles = fblocks * mblocks;
+    const uint32_t F2 = 2 * p.F;
     const uint64_t n2 = (uint64_t)p.rows * F2;
-    float d[3][4][8];                                   // dG, dU, H
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = r0 + g + 32 * i;
-        uint4 vh = make_uint4(0, 0, 0, 0), vg = vh, vu = vh;
-        if (r < p.rows && in_bounds((uint64_t)r * p.ld_dh + c, 8, pitched_extent(p.rows, p.F, p.ld_dh), p.status) &&
-            in_bounds((uint64_t)r * p.ld_gu + p.F + c, 8, pitched_extent(p.rows, F2, p.ld_gu), p.status)) {
-            vh = __ldg(reinterpret_cast<const uint4*>(p.dh + (size_t)r * p.ld_dh + c));
-            vg = __ldg(reinterpret_cast<const uint4*>(p.gu + (size_t)r * p.ld_gu + c));
-            vu = __ldg(reinterpret_cast<const uint4*>(p.gu + (size_t)r * p.ld_gu + p.F + c));
-        }
-        const uint32_t wh[4] = {vh.x, vh.y, vh.z, vh.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const auto pick = [&](const uint32_t (&w)[4]) {
-                return __uint_as_float((e & 1) ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-            };
-            const float dh = pick(wh), gate = pick(wg), up = pick(wu);
-            const Sigmoid sg = sigmoid_both(gate);
-            // products of two BF16 values are exact in FP32: they come first
-            d[0][i][e] = __fmul_rn(__fmul_rn(dh, up), __fmul_rn(sg.s, __fmaf_rn(gate, sg.one_minus, 1.0f)));
-            d[1][i][e] = __fmul_rn(__fmul_rn(dh, gate), sg.s);
-            d[2][i][e] = __fmul_rn(__fmul_rn(gate, up), sg.s);
-        }
-    }
-    // row-wise: dG and dU
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        const uint32_t kb = fb + a * fblocks;
+    const uint64_t dh_n = pitched_extent(p.rows, p.F, p.ld_dh), gu_n = pitched_extent(p.rows, F2, p.ld_gu);
+    const auto load = [&](uint32_t tile, uint32_t b) {
+        const uint32_t c = tile % fblocks * 128 + h * 8, r0 = tile / fblocks * 128 + g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t m = 0;
+            const uint32_t r = r0 + 32 * i;
+            const uint64_t at_dh = (uint64_t)r * p.ld_dh + c, at_gu = (uint64_t)r * p.ld_gu + c;
+            const bool ok = r < p.rows && in_bounds(at_dh, 8, dh_n, p.status) && in_bounds(at_gu + p.F, 8, gu_n, p.status);
+            const uint32_t dst = smem_u32(in + (b * 12 + 3 * i) * 512 + tid), bytes = ok ? 16 : 0;
+            cp_async16_zfill(dst, ok ? p.dh + at_dh : p.dh, bytes);
+            cp_async16_zfill(dst + 512 * 16, ok ? p.gu + at_gu : p.gu, bytes);
+            cp_async16_zfill(dst + 1024 * 16, ok ? p.gu + at_gu + p.F : p.gu, bytes);
+        }
+    };
+    uint32_t b = 0;
+    if (blockIdx.x < tiles) load(blockIdx.x, 0);
+    cp_async_commit();
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, b ^= 1) {
+        if (tile + gridDim.x < tiles) load(tile + gridDim.x, b ^ 1);
+        cp_async_commit();
+        cp_async_wait<1>();
+        const uint32_t fb = tile % fblocks, rb = tile / fblocks;
+        const uint32_t c = fb * 128 + h * 8, r0 = rb * 128 + g;
+        uint64_t d[3][4][4];                            // dG, dU, H: pairs of columns
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, abs_bits(d[a][i][e]));
+        for (int i = 0; i < 4; ++i) {
+            const uint4* src = in + (b * 12 + 3 * i) * 512 + tid;
+            const uint4 vh = src[0], vg = src[512], vu = src[1024];
+            const uint32_t wh[4] = {vh.x, vh.y, vh.z, vh.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
+            const auto pair = [](uint32_t w) { return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
 #pragma unroll
-            for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const Fp8Scale s = fp8_block_scale(m, p.status);
-            const uint32_t r = r0 + g + 32 * i;
-            if (r < p.rows) {
-                const float f[8] = {s.factor, s.factor, s.factor, s.factor, s.factor, s.factor, s.factor, s.factor};
-                const uint64_t at = (uint64_t)r * F2 + a * p.F + c;
-                if (in_bounds(at, 8, n2, p.status))
-                    *reinterpret_cast<uint2*>(p.row_codes + at) = fp8_codes8(d[a][i], f);
-                if (h == 0 && in_bounds((uint64_t)kb * p.rows + r, 1, (uint64_t)2 * fblocks * p.rows, p.status))
-                    p.row_scales[(size_t)kb * p.rows + r] = s.scale;
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t dh = pair(wh[e]), gate = pair(wg[e]), up = pair(wu[e]);
+                uint64_t s, om;
+                sigmoid2(gate, s, om);
+                // products of two BF16 values are exact in FP32: they come first
+                d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f))));
+                d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);
+                d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
             }
         }
-    }
-    // column-wise: dG, dU and H
+        // row-wise: dG and dU.  Lane j of a half-warp divides for the half-warp's block j (4 rows x 2).
+        float m[8];
 #pragma unroll
-    for (int a = 0; a < 3; ++a)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t m = 0;
+            for (int i = 0; i < 4; ++i) {
+                float x = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max(m, abs_bits(d[a][i][e]));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            if (lane < 16) s_max[warp][a][h * 8 + e] = m;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = f32x2_unpack(d[a][i][e]);
+                    x = amax_nan(amax_nan(x, v.x), v.y);
+                }
+                m[4 * a + i] = x;
+            }
+#pragma unroll
+        for (int o = 8; o; o >>= 1)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = amax_nan(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+        {
+            const float m0 = h & 1 ? m[1] : m[0], m1 = h & 1 ? m[3] : m[2], m2 = h & 1 ? m[5] : m[4], m3 = h & 1 ? m[7] : m[6];
+            const float x = h & 4 ? (h & 2 ? m3 : m2) : (h & 2 ? m1 : m0);
+            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), p.status);
+            const uint32_t r = r0 + 32 * (h & 3), kb = fb + ((h >> 2) & 1) * fblocks;
+            if (h < 8 && r < p.rows && in_bounds((uint64_t)kb * p.rows + r, 1, (uint64_t)2 * fblocks * p.rows, p.status))
+                p.row_scales[(size_t)kb * p.rows + r] = s.scale;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, s.factor, (lane & 16) + 4 * a + i);
+                    const uint64_t ff = f32x2_pack(f, f);
+                    const uint64_t f4[4] = {ff, ff, ff, ff};
+                    const uint32_t row = r0 + 32 * i;
+                    const uint64_t at = (uint64_t)row * F2 + a * p.F + c;
+                    if (row < p.rows && in_bounds(at, 8, n2, p.status))
+                        *reinterpret_cast<uint2*>(p.row_codes + at) = fp8_codes8(d[a][i], f4);
+                }
         }
-    __syncthreads();
-    if (threadIdx.x < 384) {
-        const uint32_t a = threadIdx.x >> 7, k = threadIdx.x & 127;
-        uint32_t m = 0;
+        // column-wise: dG, dU and H
 #pragma unroll
-        for (int w = 0; w < 16; ++w) m = max(m, s_max[w][a][k]);
-        const Fp8Scale s = fp8_block_scale(m, p.status);
-        s_factor[a][k] = s.factor;
-        const uint32_t col = fb * 128 + k;
-        if (a < 2) {
-            const uint64_t at = (uint64_t)rb * F2 + a * p.F + col;
-            if (in_bounds(at, 1, (uint64_t)mblocks * F2, p.status)) p.col_scales[at] = s.scale;
-        } else {
-            const uint64_t at = (uint64_t)rb * p.F + col;
-            if (in_bounds(at, 1, (uint64_t)mblocks * p.F, p.status)) p.h_scales[at] = s.scale;
+        for (int a = 0; a < 3; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = f32x2_unpack(d[a][i][e]);
+                    x = amax_nan(x, v.x);
+                    y = amax_nan(y, v.y);
+                }
+                x = amax_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                y = amax_nan(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+                if (lane < 16) *reinterpret_cast<float2*>(s_max + (warp * 3 + a) * 128 + h * 8 + 2 * e) = make_float2(x, y);
+            }
+        __syncthreads();
+        if (tid < 384) {
+            const uint32_t a = tid >> 7, k = tid & 127;
+            float x = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) x = amax_nan(x, s_max[(w * 3 + a) * 128 + k]);
+            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), p.status);
+            s_factor[a * 128 + k] = s.factor;
+            const uint32_t col = fb * 128 + k;
+            if (a < 2) {
+                const uint64_t at = (uint64_t)rb * F2 + a * p.F + col;
+                if (in_bounds(at, 1, (uint64_t)mblocks * F2, p.status)) p.col_scales[at] = s.scale;
+            } else {
+                const uint64_t at = (uint64_t)rb * p.F + col;
+                if (in_bounds(at, 1, (uint64_t)mblocks * p.F, p.status)) p.h_scales[at] = s.scale;
+            }
         }
-    }
-    __syncthreads();
+        __syncthreads();
 #pragma unroll
-    for (int a = 0; a < 3; ++a) {
-        float f[8];
+        for (int a = 0; a < 3; ++a) {
+            uint64_t f4[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = s_factor[a][h * 8 + e];
+            for (int e = 0; e < 4; ++e) f4[e] = *reinterpret_cast<const uint64_t*>(s_factor + a * 128 + h * 8 + 2 * e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r = r0 + g + 32 * i;
-            if (r >= p.rows) continue;
-            const uint64_t at = a < 2 ? (uint64_t)r * F2 + a * p.F + c : (uint64_t)r * p.F + c;
-            if (!in_bounds(at, 8, a < 2 ? n2 : n2 / 2, p.status)) continue;
-            *reinterpret_cast<uint2*>((a < 2 ? p.col_codes : p.h_codes) + at) = fp8_codes8(d[a][i], f);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = r0 + 32 * i;
+                const uint64_t at = a < 2 ? (uint64_t)r * F2 + a * p.F + c : (uint64_t)r * p.F + c;
+                if (r < p.rows && in_bounds(at, 8, a < 2 ? n2 : n2 / 2, p.status))
+                    *reinterpret_cast<uint2*>((a < 2 ? p.col_codes : p.h_codes) + at) = fp8_codes8(d[a][i], f4);
+            }
         }
     }
 }

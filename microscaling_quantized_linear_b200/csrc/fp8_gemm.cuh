@@ -105,6 +105,7 @@ struct Fp8PairCfg {
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
     static constexpr uint32_t B_UNIT = B_MN ? 64 : 64 * 128;            // from unit 0's B to unit 1's
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+    static_assert(EPI_WARPS + 2 + MMA_WARPS + 2 == THREADS / 32 && STAGES > 4, "plain loads: two spare warps, three stages in flight");
     static_assert((2 * STAGES + 8 + MMA_WARPS + 2 * GROUPS) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
@@ -134,16 +135,18 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
     }
 }
 
-// Stage one 128-row x 128-byte tile of a matrix whose pitch is not a multiple of
-// 16 bytes (a tensor map cannot describe it): 8-byte copies by the load warp, laid
+constexpr uint32_t kFp8PlainWarps = 3;                  // the load warp and the two without a role
+
+// Stage a third (`part`) of a 128-row x 128-byte tile of a matrix whose pitch is not
+// a multiple of 16 bytes (a tensor map cannot describe it): 8-byte copies, laid
 // out in the 128-byte swizzle that a tensor-map load would write (16-byte chunk c
 // of row r at chunk c ^ (r % 8)), zeros outside the matrix.
 __device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src, uint32_t rows, uint32_t cols, uint32_t r0,
-                                               uint32_t c0, uint32_t lane, unsigned int* status) {
+                                               uint32_t c0, uint32_t part, uint32_t lane, unsigned int* status) {
     const uint32_t c = c0 + (lane & 15) * 8;
     const uint32_t chunk = (lane & 15) >> 1, half = (lane & 1) * 8;
 #pragma unroll 8
-    for (uint32_t i = lane >> 4; i < 128; i += 2) {
+    for (uint32_t i = 2 * part + (lane >> 4); i < 128; i += 2 * kFp8PlainWarps) {
         const uint32_t r = r0 + i;
         const uint64_t at = (uint64_t)r * cols + c;
         const bool in = r < rows && c < cols && in_bounds(at, 8, (uint64_t)rows * cols, status);
@@ -206,7 +209,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full0 + 8 * s, PLAIN_A ? 3 : 1);
+            mbar_init(full0 + 8 * s, PLAIN_A ? 1 + 2 * kFp8PlainWarps : 1);
             mbar_init(empty0 + 8 * s, 2);
         }
         for (int b = 0; b < 4; ++b) {
@@ -246,8 +249,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
 
     if (warp >= C::EPI_WARPS) {
         regs_dec<C::OTHER_REGS>();
-        if (warp == C::LOAD_WARP) {
+        if (warp == C::LOAD_WARP || (PLAIN_A && warp >= C::MMA_WARP + C::MMA_WARPS)) {
             // ---------------------------------------------------------- tile loads (both CTAs)
+            const uint32_t part = warp == C::LOAD_WARP ? 0 : warp - (C::MMA_WARP + C::MMA_WARPS) + 1;
             if (PLAIN_A || lane == 0) {
             uint32_t it = 0;
             bool ok = true;
@@ -269,7 +273,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     }
                     const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
                     const int32_t k0 = (int32_t)(t * 128);
-                    if (lane == 0) {
+                    if (lane == 0 && part == 0) {
                         const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
                         if (rank == 0)
                             mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
@@ -277,19 +281,19 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                         tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
                     }
                     if (PLAIN_A) {
-                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, lane, p.status);
-                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, lane, p.status);
+                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, part, lane, p.status);
+                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, part, lane, p.status);
                         cp_async_commit();
-                        if (it > 0) {
-                            cp_async_wait<1>();
-                            publish(it - 1);
+                        if (it >= 3) {
+                            cp_async_wait<3>();
+                            publish(it - 3);
                         }
                     }
                 }
             }
-            if (PLAIN_A && it > 0) {
+            if (PLAIN_A) {
                 cp_async_wait<0>();
-                publish(it - 1);
+                for (uint32_t j = it > 3 ? it - 3 : 0; j < it; ++j) publish(j);
             }
             if (lane == 0) {
                 if (!ok) gave_up();
@@ -474,8 +478,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {             // acc[i] becomes H
                     const float2 x = f32x2_unpack(acc[i]), u = f32x2_unpack(acc[32 + i]);
-                    const float y0 = __fmul_rn(__fmul_rn(x.x, u.x), sigmoid_f32(x.x));
-                    const float y1 = __fmul_rn(__fmul_rn(x.y, u.y), sigmoid_f32(x.y));
+                    const float y0 = silu_mul(x.x, u.x), y1 = silu_mul(x.y, u.y);
                     m = max(m, max(abs_bits(y0), abs_bits(y1)));
                     acc[i] = f32x2_pack(y0, y1);
                 }

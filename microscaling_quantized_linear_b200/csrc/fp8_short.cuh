@@ -274,7 +274,7 @@ fp8_short_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             const size_t row = m0 + m;
             if (C::GATED) {
                 const float gate = v[0], up = v[C::P - 1];
-                const float y = __fmul_rn(__fmul_rn(gate, up), sigmoid_f32(gate));
+                const float y = silu_mul(gate, up);
                 const uint64_t at = row * p.ldo + col, gu_n = pitched_extent(p.M, 2 * p.C, p.ldo);
                 if (p.out && in_bounds(at, 1, gu_n, p.status) && in_bounds(at + p.C, 1, gu_n, p.status)) {
                     p.out[at] = __float2bfloat16_rn(gate);
