@@ -135,9 +135,17 @@ int launch_pair(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
     return launch(kern, 2 * (tiles < pairs ? tiles : pairs), C::THREADS, C::SMEM_BYTES, stream, 2, ma, mb, mo, p);
 }
 
+// The split of the contracted axis: the most CTAs that one wave of the device holds (`room`), at least
+// two blocks to a CTA, so that the weight streams through as many SMs as possible.
+uint32_t short_log_split(uint64_t tiles, uint64_t blocks, uint64_t room) {
+    uint32_t log = 3;
+    while (log > 0 && (tiles << log > room || blocks < 2u << log)) --log;
+    return log;
+}
+
 // Few tokens: one cluster of `split` CTAs per 128 output columns and TN tokens.
 template <int OP, int TN>
-int launch_short(const HostDevice& d, const Fp8Gemm& g, uint32_t split, nvq_stream_t stream) {
+int launch_short(const HostDevice& d, const Fp8Gemm& g, nvq_stream_t stream) {
     using C = Fp8ShortCfg<OP, TN>;
     const HostEncodeTiledFn encode = host_encoder();
     if (!encode) return NVQ_ERR_CUDA;
@@ -161,30 +169,33 @@ int launch_short(const HostDevice& d, const Fp8Gemm& g, uint32_t split, nvq_stre
     p.C = g.p.C;
     p.T = g.p.T;
     p.ldo = (uint32_t)g.ldo;
-    p.split = split;
+    const uint64_t tiles = (uint64_t)blocks_of(p.C) * ((p.M + TN - 1) / TN);
+    p.log_split = short_log_split(tiles, blocks_of(p.T), C::PER_SM == 2 ? (uint64_t)d.num_sms * 3 / 2 : d.num_sms);
     p.wait_ns = (uint32_t)host_wait_ns(kFp8WaitNs);
-    const uint32_t tiles = (uint32_t)(blocks_of(p.C) * ((p.M + TN - 1) / TN));
-    return launch(kern, tiles * split, C::THREADS, C::SMEM_BYTES, stream, split, mw, ma, p);
+    return launch(kern, (uint32_t)tiles << p.log_split, C::THREADS, C::SMEM_BYTES, stream, 1u << p.log_split, mw, ma, p);
 }
 
-// The split of the contracted axis: the most CTAs that one wave of the device holds, at least two
-// blocks to a CTA, so that the weight streams through as many SMs as possible.
-uint32_t short_split(uint64_t tiles, uint64_t blocks, uint32_t num_sms) {
-    uint32_t split = 8;
-    while (split > 1 && (tiles * split > num_sms || blocks < 2 * split)) split /= 2;
-    return split;
+// Whether a product runs on the few-tokens kernel: always up to 32 tokens; above, on tiles of 64 tokens,
+// where that is estimated faster than 256-row tiles on CTA pairs.  The estimates (ns) are fits to
+// measurements: a wave of CTA pairs takes 550 a block (4096 columns, 4096 contracted, 48 to 512 tokens:
+// 20.5 to 21.5 us), a wave of few-tokens CTAs 360 a block (gated: 1000) and 3500 (9.6 us at 48 tokens,
+// 10.3 at 128, 15.3 at 256, 31 in two waves at 384).
+bool use_short(bool gated, int64_t R, int64_t C, int64_t T, int64_t num_sms) {
+    if (R <= 32) return true;
+    const int64_t blocks = blocks_of(T), tiles = blocks_of(C) * ((R + 63) / 64);
+    const uint32_t log = short_log_split(tiles, blocks, num_sms);
+    const int64_t waves = ((tiles << log) + num_sms - 1) / num_sms, share = (blocks + (1 << log) - 1) >> log;
+    const int64_t pair_tiles = (R + 255) / 256 * (gated ? C / 128 : (C + 255) / 256), pairs = num_sms / 2;
+    return waves * (share * (gated ? 1000 : 360) + 3500) < (pair_tiles + pairs - 1) / pairs * blocks * 550 + 2500;
 }
-
-constexpr uint32_t kShortTokens = 64;
 
 template <int OP>
 int launch_gemm(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
-    if constexpr (OP == kFp8Linear || OP == kFp8Gated) {
-        if (g.p.R <= kShortTokens) {
-            const uint32_t split = short_split(blocks_of(g.p.C), blocks_of(g.p.T), d.num_sms);
-            if (g.p.R <= 16) return launch_short<OP, 16>(d, g, split, stream);
-            if (g.p.R <= 32) return launch_short<OP, 32>(d, g, split, stream);
-            return launch_short<OP, 64>(d, g, split, stream);
+    if constexpr (OP != kFp8Wgrad) {
+        if (g.p.T % 16 == 0 && use_short(OP == kFp8Gated, g.p.R, g.p.C, g.p.T, d.num_sms)) {
+            if (g.p.R <= 16) return launch_short<OP, 16>(d, g, stream);
+            if (g.p.R <= 32) return launch_short<OP, 32>(d, g, stream);
+            return launch_short<OP, 64>(d, g, stream);
         }
     }
     // dY's rows may be 8 bytes past a multiple of 16, which a tensor map cannot describe

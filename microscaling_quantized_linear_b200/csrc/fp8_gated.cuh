@@ -16,6 +16,11 @@
 
 namespace nvq {
 
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
+
 constexpr int kGatedBwdThreads = 512;
 constexpr int kGatedBwdSmem = 2 * 3 * 4 * 512 * 16 + 16 * 3 * 128 * 4 + 3 * 128 * 4;
 
@@ -33,20 +38,21 @@ struct GatedBwdParams {
 };
 
 // sigma(g) and 1 - sigma(g) of two values.  exp(-g) = 2^i 2^f with i the integer
-// nearest to -g log2(e), which is carried in two floats so that a large |g| costs
-// no precision, and 2^f, |f| <= 1/2, by its Taylor series to the seventh power (the
-// next term is below 2^-27): 0.44 units rms against 0.67 for expf and 0.97 for one
-// ex2.approx.  The reciprocal is the approximate one and a Newton step.  g is taken
-// within +-87; below, sigma (less than 2^-125) is taken as 0.
+// nearest to -g log2(e), f the rest to about 2^-25 (log2(e) in two floats, so that a
+// large |g| costs no precision), and 2^f, |f| <= 1/2, by its Taylor series to the
+// seventh power (the next term is below 2^-27): 0.44 units rms against 0.67 for
+// expf and 0.97 for one ex2.approx.  The reciprocal is the approximate one and a
+// Newton step.  WIDE takes any g: it is limited to +-87, and below, sigma (less than
+// 2^-125) is taken as 0; otherwise |g| <= 87.
+template <bool WIDE>
 __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& one_minus) {
     const auto two = [](float v) { return f32x2_pack(v, v); };
     const float2 gv = f32x2_unpack(g);
-    const uint64_t gc = f32x2_pack(fminf(fmaxf(gv.x, -87.0f), 87.0f), fminf(fmaxf(gv.y, -87.0f), 87.0f));
-    const uint64_t hi = f32x2_mul(gc, two(-1.4426950216f));
-    const uint64_t lo = f32x2_fma3(gc, two(-1.9259630e-8f), f32x2_fma3(gc, two(-1.4426950216f), f32x2_mul(hi, two(-1.0f))));
-    const uint64_t rounded = f32x2_add(hi, two(12582912.0f));       // 1.5 2^23: the integer lands in the low bits
-    const uint64_t f = f32x2_add(f32x2_fma3(f32x2_add(rounded, two(-12582912.0f)), two(-1.0f), hi), lo);
-    uint64_t p = two(1.5252733804e-5f);                             // (ln 2)^k / k!, k = 7 .. 0
+    const uint64_t gc = WIDE ? f32x2_pack(fminf(fmaxf(gv.x, -87.0f), 87.0f), fminf(fmaxf(gv.y, -87.0f), 87.0f)) : g;
+    const uint64_t i = f32x2_fma3(gc, two(-1.4426950216f), two(12582912.0f));       // 1.5 2^23: the integer lands in the low bits
+    uint64_t f = f32x2_fma3(i, two(-1.0f), two(12582912.0f));
+    f = f32x2_fma3(gc, two(-1.9259630e-8f), f32x2_fma3(gc, two(-1.4426950216f), f));
+    uint64_t p = two(1.5252733804e-5f);                                             // (ln 2)^k / k!, k = 7 .. 0
     p = f32x2_fma3(p, f, two(1.5403530394e-4f));
     p = f32x2_fma3(p, f, two(1.3333558146e-3f));
     p = f32x2_fma3(p, f, two(9.6181291076e-3f));
@@ -54,19 +60,21 @@ __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& 
     p = f32x2_fma3(p, f, two(0.2402265070f));
     p = f32x2_fma3(p, f, two(0.6931471806f));
     p = f32x2_fma3(p, f, two(1.0f));
-    const float2 pv = f32x2_unpack(p), rv = f32x2_unpack(rounded);
-    const uint64_t e = f32x2_pack(__uint_as_float(__float_as_uint(pv.x) + (__float_as_uint(rv.x) << 23)),
-                                  __uint_as_float(__float_as_uint(pv.y) + (__float_as_uint(rv.y) << 23)));
-    const uint64_t d = f32x2_add(e, two(1.0f)), neg = f32x2_fma3(e, two(-1.0f), two(-1.0f));
-    const float2 dv = f32x2_unpack(d);
+    const float2 pv = f32x2_unpack(p), iv = f32x2_unpack(i);
+    const uint64_t e = f32x2_pack(__uint_as_float(__float_as_uint(pv.x) + (__float_as_uint(iv.x) << 23)),
+                                  __uint_as_float(__float_as_uint(pv.y) + (__float_as_uint(iv.y) << 23)));
+    const uint64_t neg = f32x2_fma3(e, two(-1.0f), two(-1.0f));
+    const float2 nv = f32x2_unpack(neg);
     float rx, ry;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(dv.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(dv.y));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(-nv.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(-nv.y));
     const uint64_t r = f32x2_pack(rx, ry);
-    const uint64_t s = f32x2_fma3(r, f32x2_fma3(neg, r, two(1.0f)), r);
-    one_minus = f32x2_mul(e, s);
-    const float2 sv = f32x2_unpack(s);
-    sigma = f32x2_pack(gv.x < -87.0f ? 0.0f : sv.x, gv.y < -87.0f ? 0.0f : sv.y);
+    sigma = f32x2_fma3(r, f32x2_fma3(neg, r, two(1.0f)), r);
+    one_minus = f32x2_mul(e, sigma);
+    if (WIDE) {
+        const float2 sv = f32x2_unpack(sigma);
+        sigma = f32x2_pack(gv.x < -87.0f ? 0.0f : sv.x, gv.y < -87.0f ? 0.0f : sv.y);
+    }
 }
 
 // sigma(g) of one value in fewer registers, for the products' epilogues: ex2.approx of
@@ -118,7 +126,7 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
     const uint32_t h = lane & 15, g = tid >> 4;
     const uint32_t fblocks = p.F / 128, mblocks = (p.rows + 127) / 128, tiles = fblocks * mblocks;
     const uint32_t F2 = 2 * p.F;
-    const uint64_t n2 = (uint64_t)p.rows * F2;
+    const uint32_t n2 = p.rows * F2;                                // below 2^31
     const uint64_t dh_n = pitched_extent(p.rows, p.F, p.ld_dh), gu_n = pitched_extent(p.rows, F2, p.ld_gu);
     const auto load = [&](uint32_t tile, uint32_t b) {
         const uint32_t c = tile % fblocks * 128 + h * 8, r0 = tile / fblocks * 128 + g;
@@ -149,16 +157,20 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
             const uint4 vh = src[0], vg = src[512], vu = src[1024];
             const uint32_t wh[4] = {vh.x, vh.y, vh.z, vh.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
             const auto pair = [](uint32_t w) { return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
+            const auto values = [&](auto wide) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t dh = pair(wh[e]), gate = pair(wg[e]), up = pair(wu[e]);
-                uint64_t s, om;
-                sigmoid2(gate, s, om);
-                // products of two BF16 values are exact in FP32: they come first
-                d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f))));
-                d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);
-                d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t dh = pair(wh[e]), gate = pair(wg[e]), up = pair(wu[e]);
+                    uint64_t s, om;
+                    sigmoid2<decltype(wide)::value>(gate, s, om);
+                    // products of two BF16 values are exact in FP32: they come first
+                    d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f))));
+                    d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);
+                    d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
+                }
+            };
+            if (fold2(absmax2(absmax2(absmax2(absmax2(0, wg[0]), wg[1]), wg[2]), wg[3])) <= 0x42AEu) values(Flag<false>());   // 87
+            else values(Flag<true>());
         }
         // row-wise: dG and dU.  Lane j of a half-warp divides for the half-warp's block j (4 rows x 2).
         float m[8];
@@ -193,7 +205,7 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
                     const uint64_t ff = f32x2_pack(f, f);
                     const uint64_t f4[4] = {ff, ff, ff, ff};
                     const uint32_t row = r0 + 32 * i;
-                    const uint64_t at = (uint64_t)row * F2 + a * p.F + c;
+                    const uint32_t at = row * F2 + a * p.F + c;
                     if (row < p.rows && in_bounds(at, 8, n2, p.status))
                         *reinterpret_cast<uint2*>(p.row_codes + at) = fp8_codes8(d[a][i], f4);
                 }
@@ -240,7 +252,7 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t r = r0 + 32 * i;
-                const uint64_t at = a < 2 ? (uint64_t)r * F2 + a * p.F + c : (uint64_t)r * p.F + c;
+                const uint32_t at = a < 2 ? r * F2 + a * p.F + c : r * p.F + c;
                 if (r < p.rows && in_bounds(at, 8, a < 2 ? n2 : n2 / 2, p.status))
                     *reinterpret_cast<uint2*>((a < 2 ? p.col_codes : p.h_codes) + at) = fp8_codes8(d[a][i], f4);
             }

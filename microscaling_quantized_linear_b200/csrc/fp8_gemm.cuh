@@ -75,7 +75,8 @@ struct Fp8PairCfg {
     static constexpr bool B_MN = OP == kFp8Wgrad || OP == kFp8Dgrad;
     static constexpr bool SB_COL = OP == kFp8Wgrad;                     // one B scale per column
     static constexpr int EPI_WARPS = 8;
-    static constexpr int LOAD_WARP = EPI_WARPS, SCALE_WARP = LOAD_WARP + 1, MMA_WARP = LOAD_WARP + 2, MMA_WARPS = 4;
+    static constexpr int LOAD_WARP = EPI_WARPS, SCALE_WARP = LOAD_WARP + 1, MMA_WARP = LOAD_WARP + 2;
+    static constexpr int MMA_WARPS = PLAIN_A ? 2 : 4;                   // plain loads need the warps
     static constexpr int THREADS = 32 * (EPI_WARPS + 8);                // four warpgroups
     // registers a thread: 512 x 128 at launch, shared out 256 x 208 + 256 x 48
     static constexpr int EPI_REGS = 208, OTHER_REGS = 48;
@@ -105,7 +106,7 @@ struct Fp8PairCfg {
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
     static constexpr uint32_t B_UNIT = B_MN ? 64 : 64 * 128;            // from unit 0's B to unit 1's
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
-    static_assert(EPI_WARPS + 2 + MMA_WARPS + 2 == THREADS / 32 && STAGES > 4, "plain loads: two spare warps, three stages in flight");
+    static_assert(EPI_WARPS + 2 + MMA_WARPS + (PLAIN_A ? 3 : 0) <= THREADS / 32 && STAGES > 4, "warps; plain loads keep three stages in flight");
     static_assert((2 * STAGES + 8 + MMA_WARPS + 2 * GROUPS) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
@@ -135,22 +136,23 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
     }
 }
 
-constexpr uint32_t kFp8PlainWarps = 3;                  // the load warp and the two without a role
+constexpr uint32_t kFp8PlainWarps = 4;
 
-// Stage a third (`part`) of a 128-row x 128-byte tile of a matrix whose pitch is not
+// Stage a quarter (`part`) of a 128-row x 128-byte tile of a matrix whose pitch is not
 // a multiple of 16 bytes (a tensor map cannot describe it): 8-byte copies, laid
 // out in the 128-byte swizzle that a tensor-map load would write (16-byte chunk c
 // of row r at chunk c ^ (r % 8)), zeros outside the matrix.
 __device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src, uint32_t rows, uint32_t cols, uint32_t r0,
                                                uint32_t c0, uint32_t part, uint32_t lane, unsigned int* status) {
-    const uint32_t c = c0 + (lane & 15) * 8;
-    const uint32_t chunk = (lane & 15) >> 1, half = (lane & 1) * 8;
-#pragma unroll 8
-    for (uint32_t i = 2 * part + (lane >> 4); i < 128; i += 2 * kFp8PlainWarps) {
-        const uint32_t r = r0 + i;
-        const uint64_t at = (uint64_t)r * cols + c;
-        const bool in = r < rows && c < cols && in_bounds(at, 8, (uint64_t)rows * cols, status);
-        cp_async8_zfill(dst + i * 128 + ((chunk ^ (i & 7)) << 4) + half, in ? src + at : src, in ? 8 : 0);
+    const uint32_t i0 = 2 * part + (lane >> 4), c = c0 + (lane & 15) * 8;            // rows i0 + 8 j
+    const uint32_t live = c < cols && r0 + i0 < rows ? (rows - r0 - i0 + 7) / 8 : 0;  // of them inside
+    dst += i0 * 128 + ((((lane & 15) >> 1) ^ (i0 & 7)) << 4) + (lane & 1) * 8;
+    const uint64_t end = (uint64_t)rows * cols;
+    uint64_t at = (uint64_t)(r0 + i0) * cols + c;
+#pragma unroll
+    for (uint32_t j = 0; j < 16; ++j, at += 8 * (uint64_t)cols) {
+        const bool in = j < live && in_bounds(at, 8, end, status);
+        cp_async8_zfill(dst + j * 1024, in ? src + at : src, in ? 8 : 0);
     }
 }
 
@@ -249,9 +251,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
 
     if (warp >= C::EPI_WARPS) {
         regs_dec<C::OTHER_REGS>();
-        if (warp == C::LOAD_WARP || (PLAIN_A && warp >= C::MMA_WARP + C::MMA_WARPS)) {
+        if (warp == C::LOAD_WARP || (PLAIN_A && warp > C::THREADS / 32 - kFp8PlainWarps)) {
             // ---------------------------------------------------------- tile loads (both CTAs)
-            const uint32_t part = warp == C::LOAD_WARP ? 0 : warp - (C::MMA_WARP + C::MMA_WARPS) + 1;
+            const uint32_t part = warp == C::LOAD_WARP ? 0 : warp - (C::THREADS / 32 - kFp8PlainWarps);
             if (PLAIN_A || lane == 0) {
             uint32_t it = 0;
             bool ok = true;
@@ -351,17 +353,18 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
             cp_async_wait<0>();
         } else if (warp < C::MMA_WARP + C::MMA_WARPS) {
             // ---------------------------------------------------------- MMAs (leader), a warp per accumulator
-            // Warp m fills accumulator m: unit m % 2 of every other block, and so of every other stage.
-            static_assert(C::STAGES % 2 == 0 && C::MMA_WARPS == 4, "a warp sees every phase of its stages' barriers");
+            // Warp m fills accumulator m: unit m % 2 of every other block, and so of every other stage
+            // (two warps: both accumulators of unit m).
+            static_assert(C::STAGES % 2 == 0, "a warp sees every phase of its stages' barriers");
             if (lane == 0 && rank == 0) {
                 const uint32_t m = warp - C::MMA_WARP;
                 const uint32_t my_tiles = num_tiles > pair ? (num_tiles - pair + npairs - 1) / npairs : 0;
                 const uint32_t total = my_tiles * blocks;
                 bool ok = true;
-                for (uint32_t it = m >> 1; it < total; it += 2) {
-                    const uint32_t s = it % C::STAGES;
+                for (uint32_t it = m >> 1; it < total; it += C::MMA_WARPS / 2) {
+                    const uint32_t s = it % C::STAGES, b = (m & 1) + 2 * (it & 1);
                     if (!fp8_wait<PLAIN_A>(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag, p.wait_ns) ||
-                        (it >= 2 && !fp8_wait(tempty0 + 8 * m, ((it >> 1) - 1) & 1, abort_flag, p.wait_ns))) {
+                        (it >= 2 && !fp8_wait(tempty0 + 8 * b, ((it >> 1) - 1) & 1, abort_flag, p.wait_ns))) {
                         ok = false;
                         break;
                     }
@@ -369,9 +372,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES), bt = st + C::TILE_BYTES + (m & 1) * C::B_UNIT;
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        tc_mma_f8_pair(tmem + m * 128, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
+                        tc_mma_f8_pair(tmem + b * 128, smem_desc(st + k * C::A_STEP, 1024, 1024, 2),
                                        smem_desc(bt + k * C::B_STEP, 1024, 1024, 2), C::IDESC, k != 0);
-                    tc_commit_pair_mc(tfull0 + 8 * m, 0x3);
+                    tc_commit_pair_mc(tfull0 + 8 * b, 0x3);
                     tc_commit_pair_mc(empty0 + 8 * s, 0x3);
                 }
                 if (!ok) gave_up();
