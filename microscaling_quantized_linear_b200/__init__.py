@@ -509,9 +509,9 @@ def fp8_block_scale_shape(kind, rows, cols):
 
 def _codes(t, name, shape=None):
     """A dense matrix of E4M3 codes (uint8 or float8_e4m3fn), optionally of a given shape."""
-    if t.dtype != torch.uint8 and t.dtype != _e4m3:
+    if t.dtype is not torch.uint8 and t.dtype is not _e4m3:
         raise ValueError("%s: expected uint8 or float8_e4m3fn codes, got %s" % (name, t.dtype))
-    if t.dim() != 2 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError("%s: expected a contiguous %s, got shape %s strides %s"
                          % (name, "matrix" if shape is None else "[%d, %d] matrix" % shape, tuple(t.shape),
                             tuple(t.stride())))
@@ -519,9 +519,9 @@ def _codes(t, name, shape=None):
 
 
 def _scales(t, name, shape):
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise ValueError("%s: expected torch.float32, got %s" % (name, t.dtype))
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: expected a contiguous [%d, %d] matrix, got shape %s strides %s"
                          % (name, shape[0], shape[1], tuple(t.shape), tuple(t.stride())))
     return t
@@ -533,7 +533,7 @@ def _bf16(t, name, rows=None, cols=None):
         return t
     if t.dtype != torch.bfloat16:
         raise ValueError("%s: expected torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)) or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or (rows is not None and t.shape != (rows, cols)) or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("%s: expected a %smatrix with unit column stride, got shape %s strides %s"
                          % (name, "" if rows is None else "[%d, %d] " % (rows, cols), tuple(t.shape), tuple(t.stride())))
     return t
@@ -791,6 +791,84 @@ def fp8_block_gated_backward(dh, gate_up, stream=None):
                                          rs.data_ptr(), cc.data_ptr(), cs.data_ptr(), hc.data_ptr(), hs.data_ptr(),
                                          M, F, raw), "fp8_block_gated_backward")
     return (rc, rs), (cc, cs), (hc, hs)
+
+
+class BlockFp8Linear:
+    """A linear layer y = x . W^T + bias in FP8 with one FP32 scale per block of
+    128: the weight [N, K] (BF16) is quantized once, activations on every call.
+    Serving: layer(x).  Training: y, saved = layer.forward(x), then
+    dx, dw, db = layer.backward(dy, saved); after an optimizer step, update(w).
+    Holds the weight's codes and scales and nothing of a call, so calls may run
+    on several streams at once."""
+
+    def __init__(self, weight, bias=None):
+        self.N, self.K = weight.shape
+        self.bias = bias
+        self.w = fp8_block_quantize_weight(weight)
+
+    def update(self, weight, stream=None):
+        """Quantize a new weight into the same buffers (calls in flight on other
+        streams must have been ordered before it)."""
+        fp8_block_quantize_weight(weight, *self.w, stream=stream)
+
+    def __call__(self, x, out=None, stream=None):
+        return fp8_block_linear(*fp8_block_quantize(x, stream=stream), *self.w, bias=self.bias, out=out, stream=stream)
+
+    def forward(self, x, stream=None):
+        """(y, saved): saved is x quantized column-wise, one byte a value."""
+        codes, scales, *saved = fp8_block_quantize_both(x, stream=stream)
+        return fp8_block_linear(codes, scales, *self.w, bias=self.bias, stream=stream), tuple(saved)
+
+    def backward(self, dy, saved, dw=None, stream=None):
+        """(dx BF16, dw FP32, db FP32 or None without a bias); dw given is added to."""
+        rc, rs, cc, cs = fp8_block_quantize_both(dy, stream=stream)
+        dx = fp8_block_linear_dgrad(rc, rs, *self.w, stream=stream)
+        dw = fp8_block_linear_wgrad(cc, cs, *saved, out=dw, accumulate=dw is not None, stream=stream)
+        db = None
+        if self.bias is not None:
+            with torch.cuda.stream(stream):
+                db = dy.sum(0, dtype=torch.float32)
+        return dx, dw, db
+
+
+class BlockFp8GatedFF:
+    """A gated feed-forward block y = (SiLU(x . Wg^T) * (x . Wu^T)) . Wd^T in FP8
+    with one FP32 scale per block of 128: w_gate_up [2F, K] holds Wg above Wu, w_down
+    is [N, F], both BF16, F a multiple of 128.  Serving: ff(x), three launches.
+    Training: y, saved = ff.forward(x), then
+    dx, dw_gate_up, dw_down = ff.backward(dy, saved)."""
+
+    def __init__(self, w_gate_up, w_down):
+        if w_gate_up.shape[0] != 2 * w_down.shape[1]:
+            raise ValueError("w_gate_up: %d rows, w_down: %d columns" % (w_gate_up.shape[0], w_down.shape[1]))
+        self.w_gate_up = fp8_block_quantize_weight(w_gate_up)
+        self.w_down = fp8_block_quantize_weight(w_down)
+
+    def update(self, w_gate_up, w_down, stream=None):
+        """Quantize new weights into the same buffers."""
+        fp8_block_quantize_weight(w_gate_up, *self.w_gate_up, stream=stream)
+        fp8_block_quantize_weight(w_down, *self.w_down, stream=stream)
+
+    def __call__(self, x, out=None, stream=None):
+        codes, scales, _ = fp8_block_gated_linear(*fp8_block_quantize(x, stream=stream), *self.w_gate_up, stream=stream)
+        return fp8_block_linear(codes, scales, *self.w_down, out=out, stream=stream)
+
+    def forward(self, x, stream=None):
+        """(y, saved): saved is x quantized column-wise, and gate and up in BF16."""
+        codes, scales, cc, cs = fp8_block_quantize_both(x, stream=stream)
+        codes, scales, gate_up = fp8_block_gated_linear(codes, scales, *self.w_gate_up, save=True, stream=stream)
+        return fp8_block_linear(codes, scales, *self.w_down, stream=stream), (cc, cs, gate_up)
+
+    def backward(self, dy, saved, dw_gate_up=None, dw_down=None, stream=None):
+        """(dx BF16, dw_gate_up, dw_down FP32); gradients given are added to."""
+        cc, cs, gate_up = saved
+        rc, rs, yc, ys = fp8_block_quantize_both(dy, stream=stream)
+        dh = fp8_block_linear_dgrad(rc, rs, *self.w_down, stream=stream)
+        rows, columns, h = fp8_block_gated_backward(dh, gate_up, stream=stream)
+        dw_down = fp8_block_linear_wgrad(yc, ys, *h, out=dw_down, accumulate=dw_down is not None, stream=stream)
+        dx = fp8_block_linear_dgrad(*rows, *self.w_gate_up, stream=stream)
+        dw_gate_up = fp8_block_linear_wgrad(*columns, cc, cs, out=dw_gate_up, accumulate=dw_gate_up is not None, stream=stream)
+        return dx, dw_gate_up, dw_down
 
 
 # --------------------------------------------------------------------------- diagnostics

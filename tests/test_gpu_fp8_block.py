@@ -460,3 +460,107 @@ def test_float8_dtype_views_are_taken():
     a, w = operand(9, 256, "rows", 1, True), operand(136, 256, "tiles", 2, True)
     f8 = torch.float8_e4m3fn
     assert torch.equal(nvq.fp8_block_linear(a[0].view(f8), a[1], w[0].view(f8), w[1]), nvq.fp8_block_linear(*a, *w))
+
+
+# ------------------------------------------------------------------ layers, failure, debug build
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_linear_layer(M):
+    K, N = 272, 400
+    w, b, x, dy = randn(N, K, seed=1, std=0.05).to(CUDA), randn(N, seed=2).to(CUDA), activation(M, K, 3).to(CUDA), randn(M, N, seed=4).to(CUDA)
+    layer = nvq.BlockFp8Linear(w, b)
+    y, saved = layer.forward(x)
+    assert torch.equal(y, layer(x))
+    a = nvq.fp8_block_quantize(x)
+    assert torch.equal(y, nvq.fp8_block_linear(*a, *nvq.fp8_block_quantize_weight(w), bias=b))
+    dx, dw, db = layer.backward(dy, saved)
+    X, W, D = (t.double().cpu().numpy() for t in (x, w, dy))
+    # three quantizations' half steps: relative to the sums of magnitudes
+    q = 2 * U_E4M3 + U_E4M3 ** 2 + 2.0 ** -8
+    inside(dx.double().cpu().numpy(), D @ W, q * (np.abs(D) @ np.abs(W)) + 2.0 ** -9 * np.abs(D).max() * np.abs(W).max() * N)
+    inside(dw.double().cpu().numpy(), D.T @ X, q * (np.abs(D.T) @ np.abs(X)) + 2.0 ** -9 * np.abs(D).max() * np.abs(X).max() * M)
+    inside(db.double().cpu().numpy(), D.sum(0), M * 2.0 ** -24 * np.abs(D).sum(0))
+    again = layer.backward(dy, saved, dw=dw.clone())[1]
+    inside(again.double().cpu().numpy(), 2 * dw.double().cpu().numpy(), 2.0 ** -23 * np.abs(dw.double().cpu().numpy()))
+    layer.update(2 * w)
+    assert torch.equal(layer(x), nvq.fp8_block_linear(*a, *nvq.fp8_block_quantize_weight(2 * w), bias=b))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2, saved2 = layer.forward(x, stream=s)
+    g2 = layer.backward(dy, saved2, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y2, layer(x)) and torch.equal(g2[1], dw) and torch.equal(g2[2], db)
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_gated_ff_layer(M):
+    K, F, N = 272, 384, 256
+    wgu, wd = randn(2 * F, K, seed=1, std=0.05).to(CUDA), randn(N, F, seed=2, std=0.05).to(CUDA)
+    x, dy = activation(M, K, 3).to(CUDA), randn(M, N, seed=4).to(CUDA)
+    ff = nvq.BlockFp8GatedFF(wgu, wd)
+    y, saved = ff.forward(x)
+    assert torch.equal(y, ff(x))
+    h, hs, _ = nvq.fp8_block_gated_linear(*nvq.fp8_block_quantize(x), *nvq.fp8_block_quantize_weight(wgu))
+    assert torch.equal(y, nvq.fp8_block_linear(h, hs, *nvq.fp8_block_quantize_weight(wd)))
+    dx, dwgu, dwd = ff.backward(dy, saved)
+    # the gradients of the BF16 block, to the accuracy that E4M3 operands leave: 2-norms within 15 %
+    # (each of at most five quantizations on a path is within 2^-4 of each value)
+    p = [t.double().requires_grad_() for t in (x, wgu, wd)]
+    gu = p[0] @ p[1].t()
+    out = (torch.nn.functional.silu(gu[:, :F]) * gu[:, F:]) @ p[2].t()
+    out.backward(dy.double())
+    for got, want in zip((y, dx, dwgu, dwd), (out.detach(), p[0].grad, p[1].grad, p[2].grad)):
+        assert (got.double() - want).norm() <= 0.15 * want.norm()
+    again = ff.backward(dy, saved, dw_gate_up=dwgu.clone(), dw_down=dwd.clone())
+    assert torch.equal(again[0], dx) and torch.allclose(again[1], 2 * dwgu, rtol=2.0 ** -22, atol=0) and torch.allclose(again[2], 2 * dwd, rtol=2.0 ** -22, atol=0)
+    with pytest.raises(ValueError, match="rows"):
+        nvq.BlockFp8GatedFF(wgu, wgu)
+
+
+def test_timeout_is_reported_and_leaves_the_context_usable():
+    """With a wait limit of 1 ns a product may give up; it says so and returns, and the next is right."""
+    big = [(operand(m, 4096, "rows", 1, False), operand(4096, 4096, "tiles", 2, False)) for m in (8, 2000)]
+    want = [nvq.fp8_block_linear(*a, *w) for a, w in big]
+    assert nvq.device_status() == 0
+    for (a, w), y in zip(big, want):
+        nvq.set_wait_limit(1)
+        try:
+            nvq.fp8_block_linear(*a, *w)
+            assert nvq.device_status() in (0, nvq.NVQ_STATUS_TIMEOUT)
+        finally:
+            nvq.set_wait_limit(0)
+        assert torch.equal(nvq.fp8_block_linear(*a, *w), y)
+        assert nvq.device_status() == 0
+
+
+DEBUG_RUN = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import microscaling_quantized_linear_b200 as nvq
+import test_gpu_fp8_block as t
+assert nvq.DEBUG_BUILD
+for M, K in t.SHAPES:
+    t.test_quantize_matches_definition_bit_for_bit(M, K)
+for M, N, K in [(1, 264, 128), (17, 248, 400), (65, 264, 512), (257, 520, 144), (1000, 2056, 336)]:
+    t.test_linear(M, N, K, True)
+for M, N, K in [(1, 8, 16), (300, 1032, 272), (129, 400, 256), (700, 1296, 784)]:
+    t.test_dgrad(M, N, K, True)
+    t.test_wgrad(M, N, K, True)
+for M, F, K in [(3, 256, 144), (33, 256, 400), (300, 512, 784)]:
+    t.test_gated_linear(M, F, K, True)
+for M, F in [(1, 128), (129, 640)]:
+    t.test_gated_backward(M, F)
+assert nvq.device_status() == 0
+print("clean")
+"""
+
+
+def test_debug_build_finds_no_access_out_of_bounds():
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = subprocess.run([sys.executable, "-c", DEBUG_RUN % (os.path.dirname(here), here)], env=dict(os.environ, NVQ_DEBUG="1"),
+                         capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "clean" in out.stdout, out.stdout[-2000:] + out.stderr[-4000:]
