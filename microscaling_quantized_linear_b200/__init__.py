@@ -496,6 +496,7 @@ class QuantizedLinear:
 FP8_ROWS, FP8_COLUMNS, FP8_TILES = 0, 1, 2
 _FP8_KINDS = {"rows": FP8_ROWS, "columns": FP8_COLUMNS, "tiles": FP8_TILES}
 _e4m3 = torch.float8_e4m3fn
+_CODES = (torch.uint8, _e4m3)
 
 
 def fp8_block_scale_shape(kind, rows, cols):
@@ -529,7 +530,7 @@ def _scales(t, name, shape):
 
 def _bf16(t, name, rows=None, cols=None):
     """A row-major BF16 matrix with unit column stride; a single row may have any pitch."""
-    if t.dtype is torch.bfloat16 and t.dim() == 2 and t.stride(1) == 1 and rows is None:
+    if t.dtype is torch.bfloat16 and rows is None and t.dim() == 2 and t.is_contiguous():
         return t
     if t.dtype != torch.bfloat16:
         raise ValueError("%s: expected torch.bfloat16, got %s" % (name, t.dtype))
@@ -541,7 +542,12 @@ def _bf16(t, name, rows=None, cols=None):
 
 def _ld(t):
     # the pitch of one row (or none) is not read: give the kernel a valid one
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    return t.stride(0) if t.size(0) > 1 else (t.size(1) + 7) // 8 * 8
+
+
+def _new(like, shape, dtype, _empty=torch.empty_strided):
+    """A new dense matrix on like's device (the cheapest of torch's allocating calls)."""
+    return _empty(shape, (shape[1], 1), dtype=dtype, device=like.device)
 
 
 _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -554,11 +560,12 @@ def _here(stream, names, first, *rest):
     dev = first.get_device()
     if dev < 0:
         raise ValueError("%s: expected a CUDA tensor" % names[0])
-    for i, t in enumerate(rest):
+    for t in rest:
         if t is not None and t.get_device() != dev:
+            name = next(n for n, u in zip(names[1:], rest) if u is t)
             if not t.is_cuda:
-                raise ValueError("%s: expected a CUDA tensor" % names[i + 1])
-            raise ValueError("%s: on %s, %s on %s" % (names[i + 1], t.device, names[0], first.device))
+                raise ValueError("%s: expected a CUDA tensor" % name)
+            raise ValueError("%s: on %s, %s on %s" % (name, t.device, names[0], first.device))
     return _raw_stream(dev) if stream is None and dev == _device_now() else None
 
 
@@ -593,9 +600,9 @@ def fp8_block_quantize(x, codes=None, scales=None, stream=None):
         with _elsewhere(stream, x, codes, scales):
             return fp8_block_quantize(x, codes, scales)
     if codes is None:
-        codes = x.new_empty((M, K), dtype=torch.uint8)
+        codes = _new(x, (M, K), torch.uint8)
     if scales is None:
-        scales = x.new_empty(((K + 127) // 128, M), dtype=torch.float32)
+        scales = _new(x, ((K + 127) // 128, M), torch.float32)
     _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), codes.data_ptr(), scales.data_ptr(), None, None,
                                    raw), "fp8_block_quantize")
     return codes, scales
@@ -615,9 +622,9 @@ def fp8_block_quantize_columns(x, codes=None, scales=None, stream=None):
         with _elsewhere(stream, x, codes, scales):
             return fp8_block_quantize_columns(x, codes, scales)
     if codes is None:
-        codes = x.new_empty((M, K), dtype=torch.uint8)
+        codes = _new(x, (M, K), torch.uint8)
     if scales is None:
-        scales = x.new_empty(((M + 127) // 128, K), dtype=torch.float32)
+        scales = _new(x, ((M + 127) // 128, K), torch.float32)
     _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), None, None, codes.data_ptr(), scales.data_ptr(),
                                    raw), "fp8_block_quantize")
     return codes, scales
@@ -632,9 +639,9 @@ def fp8_block_quantize_both(x, stream=None):
     if raw is None:
         with _elsewhere(stream, x):
             return fp8_block_quantize_both(x)
-    rc, cc = x.new_empty((M, K), dtype=torch.uint8), x.new_empty((M, K), dtype=torch.uint8)
-    rs = x.new_empty(((K + 127) // 128, M), dtype=torch.float32)
-    cs = x.new_empty(((M + 127) // 128, K), dtype=torch.float32)
+    rc, cc = _new(x, (M, K), torch.uint8), _new(x, (M, K), torch.uint8)
+    rs = _new(x, ((K + 127) // 128, M), torch.float32)
+    cs = _new(x, ((M + 127) // 128, K), torch.float32)
     _check(_lib.fp8_block_quantize(x.data_ptr(), M, K, _ld(x), rc.data_ptr(), rs.data_ptr(), cc.data_ptr(),
                                    cs.data_ptr(), raw), "fp8_block_quantize")
     return rc, rs, cc, cs
@@ -655,7 +662,7 @@ def fp8_block_quantize_weight(w, codes=None, scales=None, stream=None):
         with _elsewhere(stream, w, codes, scales):
             return fp8_block_quantize_weight(w, codes, scales)
     if codes is None:
-        codes = w.new_empty((N, K), dtype=torch.uint8)
+        codes = _new(w, (N, K), torch.uint8)
     if scales is None:
         scales = w.new_empty(shape, dtype=torch.float32)
     _check(_lib.fp8_block_quantize_weight(w.data_ptr(), N, K, _ld(w), codes.data_ptr(), scales.data_ptr(), raw),
@@ -665,6 +672,13 @@ def fp8_block_quantize_weight(w, codes=None, scales=None, stream=None):
 
 def _fp8_pair(a_codes, a_scales, w_codes, w_scales, names):
     """Row-wise codes [M, T] and a tile-wise weight; returns (M, T, weight rows, weight columns)."""
+    # one expression for the usual case: a short call's time is the host's
+    if (a_codes.dtype in _CODES and w_codes.dtype in _CODES and a_codes.dim() == 2 and w_codes.dim() == 2
+            and a_codes.is_contiguous() and w_codes.is_contiguous() and a_scales.is_contiguous()
+            and w_scales.is_contiguous() and a_scales.dtype is torch.float32 and w_scales.dtype is torch.float32):
+        (M, T), (N, K) = a_codes.shape, w_codes.shape
+        if a_scales.shape == ((T + 127) >> 7, M) and w_scales.shape == ((N + 127) >> 7, (K + 127) >> 7):
+            return M, T, N, K
     _codes(a_codes, names[0] + "_codes")
     _codes(w_codes, names[1] + "_codes")
     M, T = a_codes.shape
@@ -688,11 +702,15 @@ def fp8_block_linear(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, 
     if raw is None:
         with _elsewhere(stream, a_codes, a_scales, w_codes, w_scales, bias, out):
             return fp8_block_linear(a_codes, a_scales, w_codes, w_scales, bias, out)
+    ld = N
     if out is None:
-        out = a_codes.new_empty((M, N), dtype=torch.bfloat16)
-    _check(_lib.fp8_block_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                 None if bias is None else bias.data_ptr(), out.data_ptr(), _ld(out), M, N, K,
-                                 raw), "fp8_block_linear")
+        out = _new(a_codes, (M, N), torch.bfloat16)
+    else:
+        ld = _ld(out)
+    rc = _lib.fp8_block_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                               None if bias is None else bias.data_ptr(), out.data_ptr(), ld, M, N, K, raw)
+    if rc:
+        raise NvqError(rc, "fp8_block_linear")
     return out
 
 
@@ -709,7 +727,7 @@ def fp8_block_linear_dgrad(dy_codes, dy_scales, w_codes, w_scales, out=None, str
         with _elsewhere(stream, dy_codes, dy_scales, w_codes, w_scales, out):
             return fp8_block_linear_dgrad(dy_codes, dy_scales, w_codes, w_scales, out)
     if out is None:
-        out = dy_codes.new_empty((M, K), dtype=torch.bfloat16)
+        out = _new(dy_codes, (M, K), torch.bfloat16)
     _check(_lib.fp8_block_linear_dgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), w_codes.data_ptr(),
                                        w_scales.data_ptr(), out.data_ptr(), _ld(out), M, N, K, raw),
            "fp8_block_linear_dgrad")
@@ -738,7 +756,7 @@ def fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out=None, acc
         with _elsewhere(stream, dy_codes, dy_scales, x_codes, x_scales, out):
             return fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out, accumulate)
     if out is None:
-        out = dy_codes.new_empty((N, K), dtype=torch.float32)
+        out = _new(dy_codes, (N, K), torch.float32)
     _check(_lib.fp8_block_linear_wgrad(dy_codes.data_ptr(), dy_scales.data_ptr(), x_codes.data_ptr(),
                                        x_scales.data_ptr(), out.data_ptr(), _ld(out), int(bool(accumulate)), M, N,
                                        K, raw), "fp8_block_linear_wgrad")
@@ -760,9 +778,9 @@ def fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save=False, str
     if raw is None:
         with _elsewhere(stream, a_codes, a_scales, w_codes, w_scales):
             return fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save)
-    codes = a_codes.new_empty((M, F), dtype=torch.uint8)
-    scales = a_codes.new_empty((F // 128, M), dtype=torch.float32)
-    gate_up = a_codes.new_empty((M, N), dtype=torch.bfloat16) if save else None
+    codes = _new(a_codes, (M, F), torch.uint8)
+    scales = _new(a_codes, (F // 128, M), torch.float32)
+    gate_up = _new(a_codes, (M, N), torch.bfloat16) if save else None
     _check(_lib.fp8_block_gated_linear(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
                                        w_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                        gate_up.data_ptr() if save else None, N, M, F, K, raw),
@@ -782,11 +800,11 @@ def fp8_block_gated_backward(dh, gate_up, stream=None):
     if raw is None:
         with _elsewhere(stream, dh, gate_up):
             return fp8_block_gated_backward(dh, gate_up)
-    rc, cc = dh.new_empty((2, M, 2 * F), dtype=torch.uint8).unbind(0)
-    rs = dh.new_empty(((2 * F + 127) // 128, M), dtype=torch.float32)
-    cs = dh.new_empty((MB, 2 * F), dtype=torch.float32)
-    hc = dh.new_empty((M, F), dtype=torch.uint8)
-    hs = dh.new_empty((MB, F), dtype=torch.float32)
+    rc, cc = _new(dh, (M, 2 * F), torch.uint8), _new(dh, (M, 2 * F), torch.uint8)
+    rs = _new(dh, ((2 * F + 127) // 128, M), torch.float32)
+    cs = _new(dh, (MB, 2 * F), torch.float32)
+    hc = _new(dh, (M, F), torch.uint8)
+    hs = _new(dh, (MB, F), torch.float32)
     _check(_lib.fp8_block_gated_backward(dh.data_ptr(), _ld(dh), gate_up.data_ptr(), _ld(gate_up), rc.data_ptr(),
                                          rs.data_ptr(), cc.data_ptr(), cs.data_ptr(), hc.data_ptr(), hs.data_ptr(),
                                          M, F, raw), "fp8_block_gated_backward")
