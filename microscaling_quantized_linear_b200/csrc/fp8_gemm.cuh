@@ -26,20 +26,32 @@
 // 64) of each CTA's B tile, so its 128 accumulator columns are tile columns
 // 64 h .. + 63 and 128 + 64 h .. + 63.  Tensor memory holds four units, two of
 // each h.  From an accumulator's completion to the MMA that may overwrite it lie
-// three hand-overs between threads (about 300 cycles each) and the drain; with
-// two 256-wide accumulators the tensor pipe stood idle for half of that time
-// (4608 x 12288 x 4096: 242 us against LATER us with units).
+// three hand-overs between threads (200 to 400 cycles each) and the drain; with two
+// 256-wide accumulators the tensor pipe stood idle for half of that time (906 cycles
+// a block without the multiply-adds, 727 with units; the MMAs alone take 512).
 // Warps 0-7: epilogue, warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of
-// units h = w / 4; 8: tile loads; 9: scales, by 4-byte copies into a ring of eight
-// blocks, as far ahead as the tiles (L2 answers after some 2,000 cycles while the
-// tiles stream in: reading them two blocks ahead in the epilogue cost 80 us of
-// 298); 10-13: MMAs (in the leader CTA), a warp per accumulator.  One thread spends
-// at least 86 cycles on issuing an MMA that takes the tensor pipe 64, and 130 on a
+// units h = w / 4; 8: tile loads; 9: scales, by 4-byte copies into a ring that runs
+// as far ahead as the tiles (L2 answers after some 2,000 cycles while the tiles
+// stream in: reading them two blocks ahead in the epilogue cost 80 us of 298);
+// 10-13: MMAs (in the leader CTA), a warp per accumulator.  One thread spends at
+// least 86 cycles on issuing an MMA that takes the tensor pipe 64, and 130 on a
 // commit: four MMAs and two commits alone measured 390 cycles a unit from two
 // warps, 276 from four, where the pipe needs 256.
 // The totals take 128 registers of an epilogue thread; a spill in its loop goes
 // through a first-level cache that shared memory has left almost nothing of, and
-// cost a third of the kernel's time, hence the register split.
+// cost up to a third of the kernel's time, hence the register split.
+//
+// Measured at 4608 x 12288 x 4096, values from normal ones: 230 us in short runs (2,017
+// TFLOP/s, SM clock 1.7 GHz), 276 us over seconds (1,680 TFLOP/s, at the power limit;
+// a BF16 library product reaches 1,360 there); dgrad 4608 x 4096 x 12288 224 us,
+// wgrad 357 us (its column scales are one more multiply and a shared-memory read for
+// each pair of values), gated 512 us short and 590 us with gate and up kept.
+// What bounds it is the epilogue: about 1,010 cycles a block, of which 500 drain and
+// add, 200 the scales, 100 to 200 each the accumulator's barrier and the release, and
+// 200 a tile's share of output; shared memory answers slowly beside the tensor core's
+// operand reads.  Tried and not kept: 16 epilogue warps of 64 columns (1,240 cycles), 32-byte
+// stores from registers in place of the staged tensor-map stores (1,230), the next block's
+// scales read before the last chunk is added (244 us against 230), longer chunks (spills).
 // Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
 #pragma once
 #include <cstdint>
@@ -396,6 +408,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         // 64 h + i, or 64 h + 64 + i
         const uint32_t lanes = tmem + ((32 * q) << 16);
         const uint32_t cblocks = (p.C + 127) / 128;
+        const uint32_t scales = smem_u32(smem + C::OFF_SCALE);
         // where this CTA's releases go: the leader's barriers
         const uint32_t release0 = mapa_shared(tempty0 + 8 * h, 0), release1 = mapa_shared(tempty0 + 8 * (h + 2), 0);
         uint32_t it = 0, slot = 0, sslot = 0, sphase = 0;
@@ -412,46 +425,46 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     ok = false;
                     break;
                 }
-                const float* scale = reinterpret_cast<const float*>(smem + C::OFF_SCALE + sslot * C::SLOT_BYTES);
+                const uint32_t block_scale = scales + sslot * C::SLOT_BYTES;
                 if (++sslot == (uint32_t)C::SLOTS) {
                     sslot = 0;
                     sphase ^= 1;
                 }
-                const float sa = scale[32 * q + lane];
-                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, scale[128]);
-                const float f1 = C::SB_COL ? sa : __fmul_rn(sa, scale[129]);
+                const float sa = lds_f32(block_scale + 4 * (32 * q + lane));
+                const float f0 = C::SB_COL ? sa : __fmul_rn(sa, lds_f32(block_scale + 512));
+                const float f1 = C::SB_COL ? sa : __fmul_rn(sa, lds_f32(block_scale + 516));
                 const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
                 if (!ready && !fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const auto add = [&](const uint32_t (&v)[16], int j) {
-                    const uint64_t s = j < 4 ? s0 : s1;
-                    const float4* sb = reinterpret_cast<const float4*>(scale + 128 + 64 * h + 16 * j + (j < 4 ? 0 : 64));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint64_t x = f32x2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
-                        uint64_t y = f32x2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-                        if (C::SB_COL) {
-                            const float4 c = sb[i];
-                            x = f32x2_mul(x, f32x2_pack(c.x, c.y));
-                            y = f32x2_mul(y, f32x2_pack(c.z, c.w));
-                        }
-                        f32x2_fma(acc[8 * j + 2 * i], x, s);
-                        f32x2_fma(acc[8 * j + 2 * i + 1], y, s);
-                    }
-                };
                 // a chunk's load runs while the chunk before it is added
                 const uint32_t src = lanes + b * 128;
                 uint32_t v[2][16];
+                const auto add = [&](int j) {
+                    const uint32_t(&x)[16] = v[j & 1];
+                    const uint64_t s = j < 4 ? s0 : s1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (C::SB_COL) {
+                            uint64_t c0, c1;
+                            lds_2xf32x2(block_scale + 512 + 4 * (64 * h + 16 * j + (j < 4 ? 0 : 64) + 4 * i), c0, c1);
+                            tmem_fma2(acc[8 * j + 2 * i], x[4 * i], x[4 * i + 1], c0, s);
+                            tmem_fma2(acc[8 * j + 2 * i + 1], x[4 * i + 2], x[4 * i + 3], c1, s);
+                        } else {
+                            tmem_fma2(acc[8 * j + 2 * i], x[4 * i], x[4 * i + 1], s);
+                            tmem_fma2(acc[8 * j + 2 * i + 1], x[4 * i + 2], x[4 * i + 3], s);
+                        }
+                    }
+                };
                 tc_ld_32x32b_x16(src, v[0]);
-                tc_wait_ld(v[0]);
+                tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 7; ++j) {
                     tc_ld_32x32b_x16(src + 16 * (j + 1), v[(j + 1) & 1]);
-                    add(v[j & 1], j);
-                    tc_wait_ld(v[(j + 1) & 1]);
+                    add(j);
+                    tc_wait_ld();
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -459,7 +472,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 if (lane == 0) mbar_arrive_relaxed_cluster(b == h ? release0 : release1);
                 // look at the next block's accumulator while the last chunk is added
                 ready = mbar_test(tfull0 + 8 * (b ^ 2), ((it + 1) >> 1) & 1);
-                add(v[1], 7);
+                add(7);
                 if (sslot % C::GROUP == 0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sempty0 + 8 * ((sslot == 0 ? C::GROUPS : sslot / C::GROUP) - 1));

@@ -218,7 +218,7 @@ fp8_short_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
             }
             if (!ok) continue;
             tc_fence_after();
-            const float* sc = s_scale + (C::GATED ? g * C::CHUNK * TN : 0) + jc * TN + first;
+            const uint32_t sc = smem_u32(s_scale + (C::GATED ? g * C::CHUNK * TN : 0) + jc * TN + first);
             constexpr int CS = C::NT < 16 ? 8 : 16;
 #pragma unroll
             for (int c = 0; c < C::NT; c += CS) {
@@ -228,13 +228,13 @@ fp8_short_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 } else {
                     tc_ld_32x32b_x16(lanes + b * TN + c, v);
                 }
-                tc_wait_ld(v);
+                tc_wait_ld();
 #pragma unroll
                 for (int i = 0; i < CS / 2; i += 2) {
-                    const float4 s4 = *reinterpret_cast<const float4*>(sc + c + 2 * i);
-                    f32x2_fma(acc[c / 2 + i], f32x2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f32x2_pack(s4.x, s4.y));
-                    f32x2_fma(acc[c / 2 + i + 1], f32x2_pack(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])),
-                              f32x2_pack(s4.z, s4.w));
+                    uint64_t s0, s1;
+                    lds_2xf32x2(sc + 4 * (c + 2 * i), s0, s1);
+                    tmem_fma2(acc[c / 2 + i], v[2 * i], v[2 * i + 1], s0);
+                    tmem_fma2(acc[c / 2 + i + 1], v[2 * i + 2], v[2 * i + 3], s1);
                 }
             }
             tc_fence_before();

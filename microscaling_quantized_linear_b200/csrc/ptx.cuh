@@ -272,8 +272,7 @@ __device__ __forceinline__ void tc_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 32 lanes x 16 consecutive 32-bit columns, and the wait that names the load's
-// registers, so that nothing that uses them can be moved before it.
+// 32 lanes x 16 (8) consecutive 32-bit columns.
 __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -287,19 +286,6 @@ __device__ __forceinline__ void tc_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
-}
-
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 :: "memory");
-}
-
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :: "memory");
 }
 
 // Register count of the warps of this warpgroup from here on (multiples of 8;
@@ -388,6 +374,19 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
+}
+
+// Ordered among the other volatile statements (waits, tensor-memory loads), not
+// against other memory accesses.
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// Four floats as two f32x2 pairs.
+__device__ __forceinline__ void lds_2xf32x2(uint32_t addr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 
 __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
@@ -627,6 +626,20 @@ __device__ __forceinline__ float2 f32x2_mul(float a, float b, float m) {
 // acc += p * s and p *= s on a pair of FP32 lanes (round to nearest even per lane).
 __device__ __forceinline__ void f32x2_fma(uint64_t& acc, uint64_t p, uint64_t s) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(p), "l"(s));
+}
+
+// acc += (lo, hi) * s, and acc += (lo, hi) * c * s, on registers that a tensor-memory
+// load wrote: volatile, so that they stay behind its wait.  (Naming the registers in
+// the wait instead made the compiler copy each of them: two moves for every packed
+// multiply-add.)
+__device__ __forceinline__ void tmem_fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+    asm volatile("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"
+                 : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
+}
+
+__device__ __forceinline__ void tmem_fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t c, uint64_t s) {
+    asm volatile("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tmul.rn.f32x2 x, x, %3;\n\tfma.rn.f32x2 %0, x, %4, %0;\n\t}"
+                 : "+l"(acc) : "r"(lo), "r"(hi), "l"(c), "l"(s));
 }
 
 __device__ __forceinline__ uint64_t f32x2_fma3(uint64_t a, uint64_t b, uint64_t c) {

@@ -564,3 +564,41 @@ def test_debug_build_finds_no_access_out_of_bounds():
     out = subprocess.run([sys.executable, "-c", DEBUG_RUN % (os.path.dirname(here), here)], env=dict(os.environ, NVQ_DEBUG="1"),
                          capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and "clean" in out.stdout, out.stdout[-2000:] + out.stderr[-4000:]
+
+
+CAPTURE_FIRST = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import microscaling_quantized_linear_b200 as nvq
+x = torch.randn(300, 256, device="cuda").bfloat16()
+t = torch.randn(8, 256, device="cuda").bfloat16()
+w = torch.randn(512, 256, device="cuda").bfloat16()
+def step():
+    wq = nvq.fp8_block_quantize_weight(w)
+    rc, rs, cc, cs = nvq.fp8_block_quantize_both(x)
+    h, hs, gu = nvq.fp8_block_gated_linear(rc, rs, *wq, save=True)
+    back = nvq.fp8_block_gated_backward(x, gu)
+    y = nvq.fp8_block_linear(rc, rs, *wq)
+    return [h, hs, gu, y, nvq.fp8_block_linear_dgrad(*back[0], *wq), nvq.fp8_block_linear_wgrad(*back[1], cc, cs),
+            nvq.fp8_block_linear(*nvq.fp8_block_quantize(t), *wq)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(out, step()):
+    assert torch.equal(a, b)
+assert nvq.device_status() == 0
+print("same")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """In a fresh process every entry point's first call is inside a graph capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = subprocess.run([sys.executable, "-c", CAPTURE_FIRST % (os.path.dirname(here), here)], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "same" in out.stdout, out.stdout[-2000:] + out.stderr[-4000:]
