@@ -12,7 +12,7 @@
 #include <cstdint>
 #include "debug.cuh"
 #include "fp8_quantize.cuh"
-#include "ptx.cuh"
+#include "fp8_ptx.cuh"
 
 namespace nvq {
 

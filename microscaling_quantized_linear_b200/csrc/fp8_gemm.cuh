@@ -58,7 +58,7 @@
 #include <cuda_bf16.h>
 #include "debug.cuh"
 #include "fp8_gated.cuh"
-#include "ptx.cuh"
+#include "fp8_ptx.cuh"
 
 namespace nvq {
 

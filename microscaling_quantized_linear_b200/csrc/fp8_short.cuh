@@ -22,7 +22,7 @@
 #include "debug.cuh"
 #include "fp8_gated.cuh"
 #include "fp8_gemm.cuh"
-#include "ptx.cuh"
+#include "fp8_ptx.cuh"
 
 namespace nvq {
 
