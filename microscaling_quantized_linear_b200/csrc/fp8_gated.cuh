@@ -90,8 +90,9 @@ __device__ __forceinline__ float sigmoid1(float g) {
     return g < -87.0f ? 0.0f : __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
 }
 
-// SiLU(g) * u; the argument's NaN comes through the product.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, u), sigmoid1(g)); }
+// SiLU(g) * u; the argument's NaN comes through the product.  g * sigma(g) is at most |g|, so nothing
+// overflows that the result does not.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, sigmoid1(g)), u); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

@@ -98,7 +98,7 @@ struct Fp8PairCfg {
     static_assert(32 * EPI_WARPS * EPI_REGS + 256 * OTHER_REGS <= THREADS * 128, "register split");
     static constexpr int TILE_BYTES = 128 * 128;                        // 128 rows x 128 bytes
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;                  // A and B tile of one CTA
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = PLAIN_A ? 4 : 6;                       // plain loads: one for each of their warps
     static constexpr int STAGING = 32 * 64;                             // per epilogue warp: one chunk
     // scale slot of a block: 128 row scales, then 256 column scales or the two tile scales; slots are
     // filled GROUP blocks at a time, with one barrier a group
@@ -121,7 +121,7 @@ struct Fp8PairCfg {
     static constexpr uint32_t A_STEP = A_MN ? 4096 : 32, B_STEP = B_MN ? 4096 : 32;
     static constexpr uint32_t B_UNIT = B_MN ? 64 : 64 * 128;            // from unit 0's B to unit 1's
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
-    static_assert(EPI_WARPS + 2 + MMA_WARPS + (PLAIN_A ? 3 : 0) <= THREADS / 32 && STAGES > 4, "warps; plain loads keep three stages in flight");
+    static_assert(EPI_WARPS + 2 + MMA_WARPS + (PLAIN_A ? 4 : 0) <= THREADS / 32, "warps");
     static_assert((2 * STAGES + 8 + MMA_WARPS + 2 * GROUPS) * 8 + 16 <= BAR_BYTES, "barriers");
 };
 
@@ -151,23 +151,31 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
     }
 }
 
+// Warps of plain loads, each with a stage of its own: the proxy fence that publishes
+// a stage's copies waits for all that its warp has in flight, so more than one at a
+// time would come one after the other (dgrad of 1111 x 2056 x 1552: a quarter of each
+// of six stages to a warp 24.2 us, three warps with two stages each 19.5, this 17.9).
 constexpr uint32_t kFp8PlainWarps = 4;
 
-// Stage a quarter (`part`) of a 128-row x 128-byte tile of a matrix whose pitch is not
-// a multiple of 16 bytes (a tensor map cannot describe it): 8-byte copies, laid
-// out in the 128-byte swizzle that a tensor-map load would write (16-byte chunk c
-// of row r at chunk c ^ (r % 8)), zeros outside the matrix.
+// Stage a 128-row x 128-byte tile of a matrix whose pitch is not a multiple of 16
+// bytes (a tensor map cannot describe it) with one warp: 8-byte copies, laid out
+// in the 128-byte swizzle that a tensor-map load would write (16-byte chunk c of
+// row r at chunk c ^ (r % 8)), zeros outside the matrix.
 __device__ __forceinline__ void fp8_plain_tile(uint32_t dst, const uint8_t* src, uint32_t rows, uint32_t cols, uint32_t r0,
-                                               uint32_t c0, uint32_t part, uint32_t lane, unsigned int* status) {
-    const uint32_t i0 = 2 * part + (lane >> 4), c = c0 + (lane & 15) * 8;            // rows i0 + 8 j
-    const uint32_t live = c < cols && r0 + i0 < rows ? (rows - r0 - i0 + 7) / 8 : 0;  // of them inside
-    dst += i0 * 128 + ((((lane & 15) >> 1) ^ (i0 & 7)) << 4) + (lane & 1) * 8;
+                                               uint32_t c0, uint32_t lane, unsigned int* status) {
+    const uint32_t c = c0 + (lane & 15) * 8;
     const uint64_t end = (uint64_t)rows * cols;
-    uint64_t at = (uint64_t)(r0 + i0) * cols + c;
 #pragma unroll
-    for (uint32_t j = 0; j < 16; ++j, at += 8 * (uint64_t)cols) {
-        const bool in = j < live && in_bounds(at, 8, end, status);
-        cp_async8_zfill(dst + j * 1024, in ? src + at : src, in ? 8 : 0);
+    for (uint32_t part = 0; part < 4; ++part) {
+        const uint32_t i0 = 2 * part + (lane >> 4);                                       // rows i0 + 8 j
+        const uint32_t live = c < cols && r0 + i0 < rows ? (rows - r0 - i0 + 7) / 8 : 0;  // of them inside
+        const uint32_t d = dst + i0 * 128 + ((((lane & 15) >> 1) ^ (i0 & 7)) << 4) + (lane & 1) * 8;
+        uint64_t at = (uint64_t)(r0 + i0) * cols + c;
+#pragma unroll
+        for (uint32_t j = 0; j < 16; ++j, at += 8 * (uint64_t)cols) {
+            const bool in = j < live && in_bounds(at, 8, end, status);
+            cp_async8_zfill(d + j * 1024, in ? src + at : src, in ? 8 : 0);
+        }
     }
 }
 
@@ -226,7 +234,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full0 + 8 * s, PLAIN_A ? 1 + 2 * kFp8PlainWarps : 1);
+            mbar_init(full0 + 8 * s, PLAIN_A ? 3 : 1);
             mbar_init(empty0 + 8 * s, 2);
         }
         for (int b = 0; b < 4; ++b) {
@@ -266,53 +274,30 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
 
     if (warp >= C::EPI_WARPS) {
         regs_dec<C::OTHER_REGS>();
-        if (warp == C::LOAD_WARP || (PLAIN_A && warp > C::THREADS / 32 - kFp8PlainWarps)) {
+        if (warp == C::LOAD_WARP) {
             // ---------------------------------------------------------- tile loads (both CTAs)
-            const uint32_t part = warp == C::LOAD_WARP ? 0 : warp - (C::THREADS / 32 - kFp8PlainWarps);
-            if (PLAIN_A || lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            // the plain copies of iteration j are complete: publish them to the leader's MMAs
-            const auto publish = [&](uint32_t j) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * (j % C::STAGES), 0));
-            };
-            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
-                const uint32_t cb = tile / p.row_tiles;
-                const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
-                const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
-                for (uint32_t t = 0; t < blocks; ++t, ++it) {
-                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
-                    const int32_t k0 = (int32_t)(t * 128);
-                    if (lane == 0 && part == 0) {
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                    const uint32_t cb = tile / p.row_tiles;
+                    const int32_t r0 = (int32_t)((tile % p.row_tiles) * 256 + 128 * rank);
+                    const int32_t c0 = OP == kFp8Gated ? (int32_t)(cb * 128 + rank * p.C) : (int32_t)(cb * 256 + 128 * rank);
+                    for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                        const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                        if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+                        const int32_t k0 = (int32_t)(t * 128);
                         const uint32_t fb = mapa_shared(full0 + 8 * s, 0);
                         if (rank == 0)
                             mbar_arrive_expect_tx(full0 + 8 * s, 2 * (PLAIN_A ? C::TILE_BYTES : C::STAGE_BYTES));
                         if (!PLAIN_A) tma_load_2d_pair(st, &tmap_a, fb, C::A_MN ? r0 : k0, C::A_MN ? k0 : r0);
                         tma_load_2d_pair(st + C::TILE_BYTES, &tmap_b, fb, C::B_MN ? c0 : k0, C::B_MN ? k0 : c0);
                     }
-                    if (PLAIN_A) {
-                        if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, k0, r0, part, lane, p.status);
-                        else fp8_plain_tile(st, p.a, p.R, p.T, r0, k0, part, lane, p.status);
-                        cp_async_commit();
-                        if (it >= 3) {
-                            cp_async_wait<3>();
-                            publish(it - 3);
-                        }
-                    }
                 }
-            }
-            if (PLAIN_A) {
-                cp_async_wait<0>();
-                for (uint32_t j = it > 3 ? it - 3 : 0; j < it; ++j) publish(j);
-            }
-            if (lane == 0) {
                 if (!ok) gave_up();
                 // Neither CTA leaves while a load it issued may be in flight: the leader's
                 // barriers count both CTAs' bytes; the peer learns of its own through the
@@ -321,7 +306,33 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never,
                              *abort_flag ? kFp8AbortNs : kFp8WaitNs);
             }
+        } else if (PLAIN_A && warp >= C::THREADS / 32 - kFp8PlainWarps) {
+            // ---------------------------------------------------------- plain A tiles (both CTAs)
+            static_assert(!PLAIN_A || C::STAGES % kFp8PlainWarps == 0, "a warp sees every phase of its stages' barriers");
+            uint32_t it = 0, turn = warp - (C::THREADS / 32 - kFp8PlainWarps);
+            bool ok = true;
+            for (uint32_t tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const uint32_t r0 = (tile % p.row_tiles) * 256 + 128 * rank;
+                for (uint32_t t = 0; t < blocks; ++t, ++it) {
+                    if (it != turn) continue;
+                    turn += kFp8PlainWarps;
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+                    if (C::A_MN) fp8_plain_tile(st, p.a, p.T, p.R, t * 128, r0, lane, p.status);
+                    else fp8_plain_tile(st, p.a, p.R, p.T, r0, t * 128, lane, p.status);
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    // publish the copies to the leader's MMAs
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(full0 + 8 * s, 0));
+                }
             }
+            if (!ok && lane == 0) gave_up();
         } else if (warp == C::SCALE_WARP) {
             // ---------------------------------------------------------- scales (both CTAs)
             const uint32_t cblocks = (p.C + 127) / 128;

@@ -315,6 +315,23 @@ def test_gated_linear(M, F, K, save):
     assert nvq.device_status() == 0
 
 
+@pytest.mark.parametrize("M", [3, 70])
+def test_gated_linear_whose_gate_times_up_passes_fp32(M):
+    """SiLU(gate) * up is finite where gate * up is not: -80 and -200 times 2^120."""
+    a = torch.zeros(M, 128, dtype=torch.bfloat16)
+    a[:, 0] = 1
+    w = torch.zeros(256, 128, dtype=torch.bfloat16)
+    w[:64, 0], w[64:128, 0], w[128:, 0] = -80.0, -200.0, 2.0 ** 120
+    w_codes, w_scales = nvq.fp8_block_quantize_weight(w.to(CUDA))
+    codes, scales, gu = nvq.fp8_block_gated_linear(*nvq.fp8_block_quantize(a.to(CUDA)), w_codes, w_scales, save=True)
+    gate = ref.value(w_codes, w_scales, "tiles")[:128, 0]
+    h = np.broadcast_to(ref.silu(gate) * 2.0 ** 120, (M, 128))
+    e = 2 * sigmoid_error(gate) * np.abs(h) + 2.0 ** -20 * np.abs(h)
+    assert np.abs(h).max() > 1 and nvq.device_status() == 0
+    assert torch.isfinite(scales).all()
+    inside(ref.value(codes, scales, "rows"), h, e4m3_step_bound(np.abs(h) + e, scales, "rows") + 2 * e)
+
+
 def test_gated_linear_of_zero_rows_is_zero():
     a = nvq.fp8_block_quantize(torch.zeros(70, 256, dtype=torch.bfloat16, device=CUDA))
     codes, scales, gu = nvq.fp8_block_gated_linear(*a, *operand(512, 256, "tiles", 2, False), save=True)
