@@ -462,6 +462,7 @@ NVQ_API int fp8_block_gated_linear(const uint8_t* a_codes, const float* a_scales
  * fp8_block_gated_backward -- the gradients of gate and up, and H again, as the
  * products that follow read them, in one pass:
  *   s = 1 / (1 + exp(-gate)), dgate = dH * up * s * (1 + gate * (1 - s)), dup = dH * gate * s
+ * The products dH * up, dH * gate and gate * up must lie within FP32's range.
  *
  *   dh, gate_up          BF16 [M, F] (pitch lddh) and [M, 2F] (pitch ldgu)
  *   row_codes, row_scales   out, [dgate | dup] [M, 2F] row-wise (for fp8_block_linear_dgrad with the [2F, K] weight)

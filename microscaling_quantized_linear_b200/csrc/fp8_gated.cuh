@@ -43,7 +43,8 @@ struct GatedBwdParams {
 // seventh power (the next term is below 2^-27): 0.44 units rms against 0.67 for
 // expf and 0.97 for one ex2.approx.  The reciprocal is the approximate one and a
 // Newton step.  WIDE takes any g: it is limited to +-87, and below, sigma (less than
-// 2^-125) is taken as 0; otherwise |g| <= 87.
+// 2^-125) is taken as 0; otherwise |g| <= 43, where the product of two 1 + exp(-g) is
+// below 2^125 and one reciprocal serves both (141.1 -> 138.3 us at 4608 x 12288).
 template <bool WIDE>
 __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& one_minus) {
     const auto two = [](float v) { return f32x2_pack(v, v); };
@@ -65,10 +66,17 @@ __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& 
                                   __uint_as_float(__float_as_uint(pv.y) + (__float_as_uint(iv.y) << 23)));
     const uint64_t neg = f32x2_fma3(e, two(-1.0f), two(-1.0f));
     const float2 nv = f32x2_unpack(neg);
-    float rx, ry;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(-nv.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(-nv.y));
-    const uint64_t r = f32x2_pack(rx, ry);
+    uint64_t r;
+    if (WIDE) {
+        float rx, ry;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(-nv.x));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(-nv.y));
+        r = f32x2_pack(rx, ry);
+    } else {                                             // 1 / x = y / (x y): one reciprocal for two
+        float rxy;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(rxy) : "f"(__fmul_rn(nv.x, nv.y)));
+        r = f32x2_mul(two(-rxy), f32x2_pack(nv.y, nv.x));
+    }
     sigma = f32x2_fma3(r, f32x2_fma3(neg, r, two(1.0f)), r);
     one_minus = f32x2_mul(e, sigma);
     if (WIDE) {
@@ -112,9 +120,13 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64
 
 // Persistent, one CTA per SM, over tiles of 128 rows x 128 of F; thread: rows
 // g + 32 i (i < 4) x 8 columns, its 96 results in registers.  The next tile's
-// inputs come in meanwhile (16-byte copies, each thread its own, no barrier).  HBM
-// sets the pace, 11 bytes a value, if a value costs less than about 60
-// instructions: hence packed pairs throughout.
+// inputs come in meanwhile (16-byte copies, each thread its own, no barrier).  11 bytes
+// a value move, which HBM does in 97 us at 4608 x 12288; measured 138 (4.6 TB/s).  The
+// arithmetic sets the pace, 53 instructions a value with packed pairs throughout: issue
+// slots are 60 % full, and multiply-adds (41 % of their unit), maxima (49 %) and
+// conversions take turns, as the two barriers of a tile keep the 16 warps in step.
+// Three-operand maxima changed nothing (141.1 -> 140.9 us); a second
+// CTA has no registers left, the 96 results of a thread hold them.
 __global__ void __launch_bounds__(kGatedBwdThreads, 1)
 fp8_gated_backward_kernel(const GatedBwdParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -170,7 +182,7 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
                     d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
                 }
             };
-            if (fold2(absmax2(absmax2(absmax2(absmax2(0, wg[0]), wg[1]), wg[2]), wg[3])) <= 0x42AEu) values(Flag<false>());   // 87
+            if (fold2(absmax2(absmax2(absmax2(absmax2(0, wg[0]), wg[1]), wg[2]), wg[3])) <= 0x422Cu) values(Flag<false>());   // 43
             else values(Flag<true>());
         }
         // row-wise: dG and dU.  Lane j of a half-warp divides for the half-warp's block j (4 rows x 2).
