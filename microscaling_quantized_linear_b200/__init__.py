@@ -821,6 +821,10 @@ class BlockFp8Linear:
 
     def __init__(self, weight, bias=None):
         self.N, self.K = weight.shape
+        if self.N % 8 or self.K % 16:
+            raise ValueError("weight: [%d, %d], expected a multiple of 8 by a multiple of 16" % (self.N, self.K))
+        if bias is not None:
+            _buf(bias, torch.bfloat16, 2 * self.N, "bias")
         self.bias = bias
         self.w = fp8_block_quantize_weight(weight)
 
@@ -859,6 +863,9 @@ class BlockFp8GatedFF:
     def __init__(self, w_gate_up, w_down):
         if w_gate_up.shape[0] != 2 * w_down.shape[1]:
             raise ValueError("w_gate_up: %d rows, w_down: %d columns" % (w_gate_up.shape[0], w_down.shape[1]))
+        if w_down.shape[1] % 128 or w_down.shape[0] % 8 or w_gate_up.shape[1] % 16:
+            raise ValueError("w_gate_up: [%d, %d], w_down: [%d, %d], expected [2F, K] and [N, F], F a multiple of 128, "
+                             "K of 16, N of 8" % (*w_gate_up.shape, *w_down.shape))
         self.w_gate_up = fp8_block_quantize_weight(w_gate_up)
         self.w_down = fp8_block_quantize_weight(w_down)
 

@@ -121,6 +121,18 @@ def test_binding_refuses_before_the_library():
         nvq.fp8_block_gated_backward(torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16))
 
 
+def test_layers_refuse_weights_that_no_call_could_take():
+    w = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)     # noqa: E731
+    for shape in ((12, 32), (16, 40)):
+        with pytest.raises(ValueError, match="weight"):
+            nvq.BlockFp8Linear(w(*shape))
+    with pytest.raises(ValueError, match="bias"):
+        nvq.BlockFp8Linear(w(16, 32), torch.zeros(16))
+    for gate_up, down in (((256, 40), (16, 128)), ((256, 32), (12, 128)), ((128, 32), (16, 64)), ((256, 32), (16, 256))):
+        with pytest.raises(ValueError, match="w_gate_up"):
+            nvq.BlockFp8GatedFF(w(*gate_up), w(*down))
+
+
 def test_reference_codes_agree_with_torch():
     """The tests' own E4M3 rounding against torch's cast, every code and ties."""
     v = ref.e4m3_value(np.arange(256)).astype(np.float32)

@@ -509,6 +509,30 @@ def test_linear_layer(M):
     assert torch.equal(y2, layer(x)) and torch.equal(g2[1], dw) and torch.equal(g2[2], db)
 
 
+def test_layers_take_an_empty_batch():
+    """Outputs without rows, weight gradients of zeros."""
+    layer, x = nvq.BlockFp8Linear(randn(264, 272).to(CUDA), randn(264).to(CUDA)), torch.empty(0, 272, dtype=torch.bfloat16, device=CUDA)
+    y, saved = layer.forward(x)
+    dx, dw, db = layer.backward(y, saved)
+    assert y.shape == layer(x).shape == (0, 264) and dx.shape == (0, 272) and (dw == 0).all() and (db == 0).all()
+    ff = nvq.BlockFp8GatedFF(randn(512, 272).to(CUDA), randn(264, 256).to(CUDA))
+    y, saved = ff.forward(x)
+    dx, dwgu, dwd = ff.backward(y, saved)
+    assert y.shape == ff(x).shape == (0, 264) and dx.shape == (0, 272)
+    assert dwgu.shape == (512, 272) and dwd.shape == (264, 256) and (dwgu == 0).all() and (dwd == 0).all()
+
+
+def test_linear_of_an_output_past_32_bits():
+    """70,016 x 32,776 values: offsets pass 2^31; the last rows and columns, exactly."""
+    M, N, K = 70016, 32776, 144
+    a, w = operand(M, K, "rows", 1, True), operand(N, K, "tiles", 2, True)
+    out = nvq.fp8_block_linear(*a, *w)
+    B = ref.value(*w, "tiles")
+    for i in (0, 65530, M - 40):
+        rows = ref.value(a[0][i:i + 40], a[1][:, i:i + 40].contiguous(), "rows")
+        check(out[i:i + 40], rows @ B.T, 0.0)
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_gated_ff_layer(M):
     K, F, N = 272, 384, 256
