@@ -151,6 +151,13 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
     }
 }
 
+// The same for a whole warp, with one decision: each lane reads the abort flag and the clock for itself, and
+// what follows a wait (tensor-memory loads, barriers, __syncwarp) takes every lane.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool fp8_wait_warp(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+    return __all_sync(0xFFFFFFFFu, fp8_wait<CLUSTER>(bar, parity, abort, limit_ns));
+}
+
 // Warps of plain loads, each with a stage of its own: the proxy fence that publishes
 // a stage's copies waits for all that its warp has in flight, so more than one at a
 // time would come one after the other (dgrad of 1111 x 2056 x 1552: a quarter of each
@@ -317,7 +324,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     if (it != turn) continue;
                     turn += kFp8PlainWarps;
                     const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (use > 0 && !fp8_wait(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
+                    if (use > 0 && !fp8_wait_warp(empty0 + 8 * s, (use - 1) & 1, abort_flag, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -346,7 +353,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                         const uint32_t n = it / C::GROUP;
                         if (n > 0) cp_async_arrive(sfull0 + 8 * ((n - 1) % C::GROUPS));
                         if (n >= (uint32_t)C::GROUPS &&
-                            !fp8_wait(sempty0 + 8 * (n % C::GROUPS), (n / C::GROUPS - 1) & 1, abort_flag, p.wait_ns)) {
+                            !fp8_wait_warp(sempty0 + 8 * (n % C::GROUPS), (n / C::GROUPS - 1) & 1, abort_flag, p.wait_ns)) {
                             ok = false;
                             break;
                         }
@@ -432,7 +439,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
             uint64_t acc[64] = {};                          // columns 2i, 2i + 1 of the unit
             for (uint32_t t = 0; t < blocks; ++t, ++it) {
                 const uint32_t b = h + 2 * (it & 1);
-                if (sslot % C::GROUP == 0 && !fp8_wait(sfull0 + 8 * (sslot / C::GROUP), sphase, abort_flag, p.wait_ns)) {
+                if (sslot % C::GROUP == 0 && !fp8_wait_warp(sfull0 + 8 * (sslot / C::GROUP), sphase, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -445,7 +452,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 const float f0 = C::SB_COL ? sa : __fmul_rn(sa, lds_f32(block_scale + 512));
                 const float f1 = C::SB_COL ? sa : __fmul_rn(sa, lds_f32(block_scale + 516));
                 const uint64_t s0 = f32x2_pack(f0, f0), s1 = f32x2_pack(f1, f1);
-                if (!ready && !fp8_wait(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
+                if (!ready && !fp8_wait_warp(tfull0 + 8 * b, (it >> 1) & 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -481,8 +488,10 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 __syncwarp();
                 // the loads have returned, and the signal publishes no memory writes
                 if (lane == 0) mbar_arrive_relaxed_cluster(b == h ? release0 : release1);
-                // look at the next block's accumulator while the last chunk is added
-                ready = mbar_test(tfull0 + 8 * (b ^ 2), ((it + 1) >> 1) & 1);
+                // look at the next block's accumulator while the last chunk is added (the votes here and in the waits
+                // cost 1 to 2 % of the kernel; one in the wait itself, ready or not, 2 to 3 %; going on after a lost wait
+                // and voting once a group of scales 2 to 5 %)
+                ready = __all_sync(0xFFFFFFFFu, mbar_test(tfull0 + 8 * (b ^ 2), ((it + 1) >> 1) & 1));
                 add(7);
                 if (sslot % C::GROUP == 0) {
                     __syncwarp();

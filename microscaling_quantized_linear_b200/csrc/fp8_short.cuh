@@ -213,8 +213,8 @@ fp8_short_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                 named_barrier_sync(1, 256);
             }
             const uint32_t u = j * C::P + (C::GATED ? g : 0), b = u % C::NBUF;
-            // every lane comes to the barriers above, so a wait that gives up ends the loop for all
-            if (ok && !fp8_wait(tfull0 + 8 * b, (u / C::NBUF) & 1, abort_flag, p.wait_ns)) {
+            // every warp comes to the barriers above, whether its wait has given up or not
+            if (ok && !fp8_wait_warp(tfull0 + 8 * b, (u / C::NBUF) & 1, abort_flag, p.wait_ns)) {
                 ok = false;
                 if (lane == 0) gave_up();
             }

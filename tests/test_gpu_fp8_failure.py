@@ -1,0 +1,71 @@
+"""Waits of the FP8 block-scaled products that run out, without a fault.
+
+nvq_set_wait_limit shortens the bounded waits between a kernel's roles, so that
+some of them give up in the middle of a product.  Every call has to return and
+leave the context usable: the status word says what happened, and the next call,
+at the default limit, gives the bits that it gave before.
+"""
+import pytest
+import torch
+
+import microscaling_quantized_linear_b200 as nvq
+
+pytestmark = pytest.mark.gpu
+
+
+def quantized(kind, rows, cols, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    return {"rows": nvq.fp8_block_quantize, "columns": nvq.fp8_block_quantize_columns,
+            "tiles": nvq.fp8_block_quantize_weight}[kind](x)
+
+
+def linear(M, N, K):
+    a, w = quantized("rows", M, K, 1), quantized("tiles", N, K, 2)
+    return lambda: [nvq.fp8_block_linear(*a, *w)]
+
+
+def dgrad(M, N, K):
+    dy, w = quantized("rows", M, N, 1), quantized("tiles", N, K, 2)
+    return lambda: [nvq.fp8_block_linear_dgrad(*dy, *w)]
+
+
+def wgrad(M, N, K):
+    dy, x = quantized("columns", M, N, 1), quantized("columns", M, K, 2)
+    return lambda: [nvq.fp8_block_linear_wgrad(*dy, *x)]
+
+
+def gated(M, F, K):
+    a, w = quantized("rows", M, K, 1), quantized("tiles", 2 * F, K, 2)
+    return lambda: list(nvq.fp8_block_gated_linear(*a, *w, save=True))
+
+
+# few tokens (clusters that split the contracted axis); CTA pairs with a tile's loads all issued at once
+# (four blocks) and with more blocks than stages; loads without a tensor map (N = 8 mod 16)
+CALLS = [(linear, 8, 4096, 4096), (linear, 48, 4096, 4096), (dgrad, 8, 4096, 4096), (gated, 3, 4096, 4096),
+         (linear, 2000, 4096, 512), (linear, 1000, 4096, 4096), (dgrad, 1000, 512, 4096), (dgrad, 1000, 4096, 2048),
+         (dgrad, 700, 2056, 1552), (wgrad, 512, 4096, 2048), (wgrad, 2048, 1024, 2048), (wgrad, 1111, 2056, 1552)]
+
+
+def limited(call, limit_ns):
+    """The status of a call whose waits are limited; its outputs are unspecified if one ran out."""
+    nvq.set_wait_limit(limit_ns)
+    try:
+        call()
+        return nvq.device_status()
+    finally:
+        nvq.set_wait_limit(0)
+
+
+def same_bits(xs, ys):
+    return all(torch.equal(x, y) for x, y in zip(xs, ys))
+
+
+@pytest.mark.parametrize("make,M,N,K", CALLS, ids=lambda v: v.__name__ if callable(v) else str(v))
+def test_products_return_when_their_waits_run_out(make, M, N, K):
+    call = make(M, N, K)
+    want = call()
+    assert nvq.device_status() == 0
+    for limit_ns in (1, 2000):
+        assert limited(call, limit_ns) in (0, nvq.NVQ_STATUS_TIMEOUT)
+        assert same_bits(call(), want) and nvq.device_status() == 0
