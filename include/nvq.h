@@ -493,7 +493,10 @@ NVQ_API const char* nvq_status_string(int code);
  * waits run out on purpose and check that the kernel reports
  * NVQ_STATUS_TIMEOUT and returns, with the context intact.  The waits with
  * which a kernel drains its own copies and tensor-core work before it exits
- * keep their 4 s limit.  Launches already issued are not affected.
+ * keep their 4 s limit, with one exception: in the FP8 products on CTA pairs a
+ * CTA that has given up waits 10 ms for the copies of each of its stages (the
+ * other CTA's share of a stage may never come).  Launches already issued are
+ * not affected.
  */
 NVQ_API int nvq_set_wait_limit(uint64_t limit_ns);
 

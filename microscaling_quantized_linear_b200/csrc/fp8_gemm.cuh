@@ -65,8 +65,8 @@ namespace nvq {
 enum Fp8Op { kFp8Linear = 0, kFp8Dgrad = 1, kFp8Wgrad = 2, kFp8Gated = 3 };
 
 constexpr uint32_t kFp8WaitNs = 4000000000u;            // 4 s per pipeline wait
-// What a load in flight is given after an abort, when its barrier's other arrivals may never come: a
-// thousand times what it takes to land.
+// What a load in flight is given once its CTA has aborted, when its barrier's other arrivals may never come:
+// a thousand times what it takes to land.  Without an abort it has the full limit.
 constexpr uint32_t kFp8AbortNs = 10000000u;
 
 struct Fp8GemmParams {
@@ -309,9 +309,11 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 // Neither CTA leaves while a load it issued may be in flight: the leader's
                 // barriers count both CTAs' bytes; the peer learns of its own through the
                 // commits of the MMAs that consumed them.
-                for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                    fp8_wait((rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), (j / C::STAGES) & 1, never,
-                             *abort_flag ? kFp8AbortNs : kFp8WaitNs);
+                for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
+                    const uint32_t bar = (rank == 0 ? full0 : empty0) + 8 * (j % C::STAGES), phase = (j / C::STAGES) & 1;
+                    // an abort, at its start or on the way, leaves it kFp8AbortNs
+                    if (!fp8_wait(bar, phase, abort_flag, kFp8WaitNs)) fp8_wait(bar, phase, never, kFp8AbortNs);
+                }
             }
         } else if (PLAIN_A && warp >= C::THREADS / 32 - kFp8PlainWarps) {
             // ---------------------------------------------------------- plain A tiles (both CTAs)

@@ -5,6 +5,8 @@ some of them give up in the middle of a product.  Every call has to return and
 leave the context usable: the status word says what happened, and the next call,
 at the default limit, gives the bits that it gave before.
 """
+import time
+
 import pytest
 import torch
 
@@ -69,3 +71,18 @@ def test_products_return_when_their_waits_run_out(make, M, N, K):
     for limit_ns in (1, 2000):
         assert limited(call, limit_ns) in (0, nvq.NVQ_STATUS_TIMEOUT)
         assert same_bits(call(), want) and nvq.device_status() == 0
+
+
+@pytest.mark.parametrize("make,M,N,K", [(linear, 2000, 4096, 512), (linear, 1000, 4096, 4096), (dgrad, 700, 2056, 1552),
+                                        (wgrad, 1111, 2056, 1552)], ids=lambda v: v.__name__ if callable(v) else str(v))
+def test_a_product_that_gives_up_returns_soon(make, M, N, K):
+    """No CTA of a pair drains its loads for seconds after the other gave up: 10 ms for each of at most six
+    stages, and a tenth of a second for all else."""
+    call = make(M, N, K)
+    want = call()
+    torch.cuda.synchronize()
+    for limit_ns in (1, 500, 1000, 2000, 4000):
+        start = time.monotonic()
+        limited(call, limit_ns)
+        assert time.monotonic() - start < 6 * 0.01 + 0.1
+    assert same_bits(call(), want) and nvq.device_status() == 0
