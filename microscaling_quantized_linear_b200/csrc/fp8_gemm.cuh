@@ -127,10 +127,14 @@ struct Fp8PairCfg {
 
 // Bounded wait of the pipeline: gives up after limit_ns or when *abort is set.
 // The clock is read on every 64th attempt only (each attempt suspends the
-// thread for a while), so a wait that is about to end costs no timer reads.
+// thread for a while), so a wait that is about to end costs no timer reads;
+// where the limit is shorter than those attempts may take, on every one.
+constexpr uint64_t kFp8ShortLimitNs = 1000000u;
+
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
     uint64_t t0 = 0;
+    const uint32_t mask = limit_ns < kFp8ShortLimitNs ? 0 : 63;
     for (uint32_t n = 0;; ++n) {
         uint32_t ok;
         if (CLUSTER)
@@ -142,7 +146,7 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
         else
             ok = mbar_try_wait(bar, parity);
         if (ok) return true;
-        if ((n & 63) == 63) {
+        if ((n & mask) == mask) {
             if (*abort) return false;
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;

@@ -86,3 +86,14 @@ def test_a_product_that_gives_up_returns_soon(make, M, N, K):
         limited(call, limit_ns)
         assert time.monotonic() - start < 6 * 0.01 + 0.1
     assert same_bits(call(), want) and nvq.device_status() == 0
+
+
+@pytest.mark.parametrize("make,M,N,K", CALLS, ids=lambda v: v.__name__ if callable(v) else str(v))
+def test_a_wait_of_one_nanosecond_runs_out_and_is_reported(make, M, N, K):
+    """The first wait for operands from memory takes longer than that in every kernel."""
+    call = make(M, N, K)
+    want = call()
+    assert nvq.device_status() == 0
+    assert limited(call, 1) == nvq.NVQ_STATUS_TIMEOUT
+    assert nvq.device_status() == 0                        # read clears it
+    assert same_bits(call(), want) and nvq.device_status() == 0
