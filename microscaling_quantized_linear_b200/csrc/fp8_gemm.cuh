@@ -504,10 +504,10 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     if (lane == 0) mbar_arrive(sempty0 + 8 * ((sslot == 0 ? C::GROUPS : sslot / C::GROUP) - 1));
                 }
             }
-            if (!ok) break;
+            if (OP != kFp8Gated && !ok) break;
             if (OP == kFp8Gated) {
                 const uint64_t h_n = (uint64_t)p.R * p.C;
-                if (p.save && rw < p.R) {
+                if (ok && p.save && rw < p.R) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t o[16];
@@ -528,12 +528,20 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     m = max(m, max(abs_bits(y0), abs_bits(y1)));
                     acc[i] = f32x2_pack(y0, y1);
                 }
-                // The row's block of 128 columns is shared by the two warps of this lane quarter.
+                // The row's block of 128 columns is shared by the two warps of this lane quarter.  They wait for
+                // different accumulators, so one may have given up where the other has not: it says so in place of
+                // its maximum, both come to the barrier once a tile and leave after the same one.
+                constexpr uint32_t kGaveUp = 0xFFFFFFFFu;  // magnitudes are below 2^31
                 uint32_t* am = s_amax + 256 * slot + 32 * q + lane;
-                am[128 * h] = m;
+                am[128 * h] = ok ? m : kGaveUp;
                 named_barrier_sync(1 + q, 64);
-                m = max(m, am[128 * (h ^ 1)]);
+                const uint32_t other = am[128 * (h ^ 1)];
                 slot ^= 1;                                 // the next tile's writes may pass this one's reads
+                if (!ok || __any_sync(0xFFFFFFFFu, other == kGaveUp)) {
+                    ok = false;
+                    break;
+                }
+                m = max(m, other);
                 if (r < p.R) {
                     const Fp8Scale s = fp8_block_scale(m, p.status);
                     const uint64_t at = (uint64_t)r * p.C + n0 + 64 * h;

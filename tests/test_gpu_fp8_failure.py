@@ -46,7 +46,7 @@ def gated(M, F, K):
 # (four blocks) and with more blocks than stages; loads without a tensor map (N = 8 mod 16)
 CALLS = [(linear, 8, 4096, 4096), (linear, 48, 4096, 4096), (dgrad, 8, 4096, 4096), (gated, 3, 4096, 4096),
          (linear, 2000, 4096, 512), (linear, 1000, 4096, 4096), (dgrad, 1000, 512, 4096), (dgrad, 1000, 4096, 2048),
-         (dgrad, 700, 2056, 1552), (wgrad, 512, 4096, 2048), (wgrad, 2048, 1024, 2048), (wgrad, 1111, 2056, 1552)]
+         (dgrad, 700, 2056, 1552), (gated, 700, 1024, 512), (gated, 2000, 4096, 512), (gated, 1111, 1408, 2048), (wgrad, 512, 4096, 2048), (wgrad, 2048, 1024, 2048), (wgrad, 1111, 2056, 1552)]
 
 
 def limited(call, limit_ns):
@@ -74,7 +74,7 @@ def test_products_return_when_their_waits_run_out(make, M, N, K):
 
 
 @pytest.mark.parametrize("make,M,N,K", [(linear, 2000, 4096, 512), (linear, 1000, 4096, 4096), (dgrad, 700, 2056, 1552),
-                                        (wgrad, 1111, 2056, 1552)], ids=lambda v: v.__name__ if callable(v) else str(v))
+                                        (gated, 2000, 4096, 512), (wgrad, 1111, 2056, 1552)], ids=lambda v: v.__name__ if callable(v) else str(v))
 def test_a_product_that_gives_up_returns_soon(make, M, N, K):
     """No CTA of a pair drains its loads for seconds after the other gave up: 10 ms for each of at most six
     stages, and a tenth of a second for all else."""
@@ -96,4 +96,18 @@ def test_a_wait_of_one_nanosecond_runs_out_and_is_reported(make, M, N, K):
     assert nvq.device_status() == 0
     assert limited(call, 1) == nvq.NVQ_STATUS_TIMEOUT
     assert nvq.device_status() == 0                        # read clears it
+    assert same_bits(call(), want) and nvq.device_status() == 0
+
+
+@pytest.mark.parametrize("M,F,K", [(300, 256, 1024), (2000, 4096, 512), (600, 1408, 4096)])
+def test_gated_warps_that_share_a_row_leave_together(M, F, K):
+    """The two warps of a row's block meet at a barrier and wait for different accumulators before it: limits
+    around the time of a stage make one give up where the other does not, at tiles early and late."""
+    call = gated(M, F, K)
+    want = call()
+    seen = set()
+    for limit_ns in (200, 500, 800, 1200, 1600, 2400, 3200, 5000):
+        for _ in range(3):
+            seen.add(limited(call, limit_ns))
+    assert nvq.NVQ_STATUS_TIMEOUT in seen and seen <= {0, nvq.NVQ_STATUS_TIMEOUT}
     assert same_bits(call(), want) and nvq.device_status() == 0
