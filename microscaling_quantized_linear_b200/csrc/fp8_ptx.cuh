@@ -105,7 +105,7 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
         :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// acc += (lo, hi) * s, and acc += (lo, hi) * c * s, on registers that a tensor-memory
+// acc += (lo, hi) * s, and acc += (lo, hi) * (c * s), on registers that a tensor-memory
 // load wrote: volatile, so that they stay behind its wait.  (Naming the registers in
 // the wait instead made the compiler copy each of them: two moves for every packed
 // multiply-add.)
@@ -115,7 +115,7 @@ __device__ __forceinline__ void tmem_fma2(uint64_t& acc, uint32_t lo, uint32_t h
 }
 
 __device__ __forceinline__ void tmem_fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t c, uint64_t s) {
-    asm volatile("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tmul.rn.f32x2 x, x, %3;\n\tfma.rn.f32x2 %0, x, %4, %0;\n\t}"
+    asm volatile("{\n\t.reg .b64 x, f;\n\tmul.rn.f32x2 f, %3, %4;\n\tmov.b64 x, {%1, %2};\n\tfma.rn.f32x2 %0, x, f, %0;\n\t}"
                  : "+l"(acc) : "r"(lo), "r"(hi), "l"(c), "l"(s));
 }
 
