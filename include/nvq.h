@@ -448,6 +448,7 @@ NVQ_API int fp8_block_linear_wgrad(const uint8_t* dy_codes, const float* dy_scal
  * fp8_block_gated_linear -- the first half of a gated feed-forward block in one
  * kernel: gate = A . Wg^T, up = A . Wu^T, H = SiLU(gate) * up, with
  * SiLU(g) = g / (1 + exp(-g)), H quantized row-wise for the second projection.
+ * Below -87, where 1 / (1 + exp(-g)) is less than 2^-125, SiLU(g) is 0.
  *
  *   a_codes, a_scales  [M, K] row-wise
  *   w_codes, w_scales  [2F, K] tile-wise: rows 0 .. F-1 are Wg, F .. 2F-1 are Wu; F a multiple of 128
@@ -462,7 +463,8 @@ NVQ_API int fp8_block_gated_linear(const uint8_t* a_codes, const float* a_scales
  * fp8_block_gated_backward -- the gradients of gate and up, and H again, as the
  * products that follow read them, in one pass:
  *   s = 1 / (1 + exp(-gate)), dgate = dH * up * s * (1 + gate * (1 - s)), dup = dH * gate * s
- * The products dH * up, dH * gate and gate * up must lie within FP32's range.
+ * s of gates below -87 and 1 - s of gates above 87, less than 2^-125, are 0.  Any finite inputs are taken: a
+ * result is infinite where it passes FP32's range itself, not where a factor of it does.
  *
  *   dh, gate_up          BF16 [M, F] (pitch lddh) and [M, 2F] (pitch ldgu)
  *   row_codes, row_scales   out, [dgate | dup] [M, 2F] row-wise (for fp8_block_linear_dgrad with the [2F, K] weight)

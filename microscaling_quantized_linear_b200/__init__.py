@@ -766,8 +766,9 @@ def fp8_block_linear_wgrad(dy_codes, dy_scales, x_codes, x_scales, out=None, acc
 def fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save=False, stream=None):
     """H = SiLU(A . Wg^T) * (A . Wu^T) in one kernel, quantized row-wise:
     (codes u8 [M, F], scales f32 [F / 128, M], gate and up).  W [2F, K]
-    tile-wise holds Wg above Wu, F a multiple of 128.  The last is None, or with
-    save=True BF16 [M, 2F] for fp8_block_gated_backward."""
+    tile-wise holds Wg above Wu, F a multiple of 128.  SiLU of a gate below -87
+    is 0.  The last is None, or with save=True BF16 [M, 2F] for
+    fp8_block_gated_backward."""
     M, K, N, Kw = _fp8_pair(a_codes, a_scales, w_codes, w_scales, ("a", "w"))
     if K != Kw:
         raise ValueError("a_codes has %d columns, w_codes %d" % (K, Kw))
@@ -791,7 +792,8 @@ def fp8_block_gated_linear(a_codes, a_scales, w_codes, w_scales, save=False, str
 def fp8_block_gated_backward(dh, gate_up, stream=None):
     """The backward pass of SiLU(gate) * up in one pass: from dH BF16 [M, F] and
     gate and up BF16 [M, 2F], ((codes, scales) of [dgate | dup] row-wise, the
-    same column-wise, (codes, scales) of H column-wise)."""
+    same column-wise, (codes, scales) of H column-wise).  Any finite inputs:
+    a result is infinite only where it passes FP32's range itself."""
     _bf16(dh, "dh")
     M, F = dh.shape
     _bf16(gate_up, "gate_up", M, 2 * F)

@@ -22,7 +22,7 @@ struct Flag {
 };
 
 constexpr int kGatedBwdThreads = 512;
-constexpr int kGatedBwdSmem = 2 * 3 * 4 * 512 * 16 + 16 * 3 * 128 * 4 + 3 * 128 * 4;
+constexpr int kGatedBwdSmem = 2 * 3 * 4 * 512 * 16 + 16 * 3 * 128 * 4 + 3 * 128 * 4 + 16;
 
 struct GatedBwdParams {
     const uint16_t* dh;         // [rows, F], pitch ld_dh
@@ -42,8 +42,8 @@ struct GatedBwdParams {
 // large |g| costs no precision), and 2^f, |f| <= 1/2, by its Taylor series to the
 // seventh power (the next term is below 2^-27): 0.44 units rms against 0.67 for
 // expf and 0.97 for one ex2.approx.  The reciprocal is the approximate one and a
-// Newton step.  WIDE takes any g: it is limited to +-87, and below, sigma (less than
-// 2^-125) is taken as 0; otherwise |g| <= 43, where the product of two 1 + exp(-g) is
+// Newton step.  WIDE takes any g: it is limited to +-87, and beyond, the smaller of the two (less than
+// 2^-125) is taken as 0, so that no large g brings it back; otherwise |g| <= 43, where the product of two 1 + exp(-g) is
 // below 2^125 and one reciprocal serves both (141.1 -> 138.3 us at 4608 x 12288).
 template <bool WIDE>
 __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& one_minus) {
@@ -82,6 +82,8 @@ __device__ __forceinline__ void sigmoid2(uint64_t g, uint64_t& sigma, uint64_t& 
     if (WIDE) {
         const float2 sv = f32x2_unpack(sigma);
         sigma = f32x2_pack(gv.x < -87.0f ? 0.0f : sv.x, gv.y < -87.0f ? 0.0f : sv.y);
+        const float2 ov = f32x2_unpack(one_minus);
+        one_minus = f32x2_pack(gv.x > 87.0f ? 0.0f : ov.x, gv.y > 87.0f ? 0.0f : ov.y);
     }
 }
 
@@ -103,6 +105,14 @@ __device__ __forceinline__ float sigmoid1(float g) {
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, sigmoid1(g)), u); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// a * b * f, f at most 1.1, where a * b may pass FP32's range though the result does not.  Both are at least 1
+// then (BF16 ends at 2^128): their product is taken 2^-128 times as large, exactly, and brought back last.
+__device__ __forceinline__ float careful_mul(float a, float b, float f) {
+    const float p = __fmul_rn(a, b);
+    if (abs_bits(p) < 0x7F800000u) return __fmul_rn(p, f);
+    return __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(a, 0x1p-64f), __fmul_rn(b, 0x1p-64f)), f), 0x1p64f), 0x1p64f);
+}
 
 // The larger magnitude, NaN if either is.
 __device__ __forceinline__ float amax_nan(float m, float v) {
@@ -127,14 +137,17 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64
 // conversions take turns, as the two barriers of a tile keep the 16 warps in step.
 // Three-operand maxima changed nothing (141.1 -> 140.9 us); a second
 // CTA has no registers left, the 96 results of a thread hold them.
-__global__ void __launch_bounds__(kGatedBwdThreads, 1)
-fp8_gated_backward_kernel(const GatedBwdParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
+//
+// A product of two BF16 values is exact in FP32, so it comes first.  It may pass FP32's range though the result does
+// not: a CTA that met a result which is not finite goes through its tiles once more (AGAIN), carefully in the octets
+// where that is so, and the others give the same bits.  (Looking at the inputs' magnitudes first cost every tile 3 %,
+// doing such a tile again inside the loop 17 %, by its spills.)
+template <bool AGAIN>
+__device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, uint8_t* smem) {
     uint4* in = reinterpret_cast<uint4*>(smem);                     // [2][12][512]
     float* s_max = reinterpret_cast<float*>(smem + 2 * 12 * 512 * 16);          // [16 warps][3][128]
     float* s_factor = s_max + 16 * 3 * 128;                                     // [3][128]
-    griddep_wait();
-    griddep_launch();
+    int* s_again = reinterpret_cast<int*>(s_factor + 3 * 128);
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t h = lane & 15, g = tid >> 4;
     const uint32_t fblocks = p.F / 128, mblocks = (p.rows + 127) / 128, tiles = fblocks * mblocks;
@@ -170,20 +183,37 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
             const uint4 vh = src[0], vg = src[512], vu = src[1024];
             const uint32_t wh[4] = {vh.x, vh.y, vh.z, vh.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
             const auto pair = [](uint32_t w) { return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
-            const auto values = [&](auto wide) {
+            const auto values = [&](auto wide, auto careful) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint64_t dh = pair(wh[e]), gate = pair(wg[e]), up = pair(wu[e]);
                     uint64_t s, om;
                     sigmoid2<decltype(wide)::value>(gate, s, om);
-                    // products of two BF16 values are exact in FP32: they come first
-                    d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f))));
-                    d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);
-                    d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
+                    const uint64_t f = f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f)));
+                    if (decltype(careful)::value) {
+                        const float2 h = f32x2_unpack(dh), u = f32x2_unpack(up), fv = f32x2_unpack(f);
+                        const uint64_t silu = f32x2_mul(gate, s);                   // at most |gate|
+                        d[0][i][e] = f32x2_pack(careful_mul(h.x, u.x, fv.x), careful_mul(h.y, u.y, fv.y));
+                        d[1][i][e] = f32x2_mul(dh, silu);
+                        d[2][i][e] = f32x2_mul(up, silu);
+                    } else {
+                        d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f);
+                        d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);
+                        d[2][i][e] = f32x2_mul(f32x2_mul(gate, up), s);
+                    }
                 }
             };
-            if (fold2(absmax2(absmax2(absmax2(absmax2(0, wg[0]), wg[1]), wg[2]), wg[3])) <= 0x422Cu) values(Flag<false>());   // 43
-            else values(Flag<true>());
+            if (fold2(absmax2(absmax2(absmax2(absmax2(0, wg[0]), wg[1]), wg[2]), wg[3])) <= 0x422Cu) values(Flag<false>(), Flag<false>());   // 43
+            else values(Flag<true>(), Flag<false>());
+            if (AGAIN) {
+                float x = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 12; ++e) {
+                    const float2 v = f32x2_unpack(d[e / 4][i][e % 4]);
+                    x = amax_nan(amax_nan(x, v.x), v.y);
+                }
+                if (abs_bits(x) >= 0x7F800000u) values(Flag<true>(), Flag<true>());
+            }
         }
         // row-wise: dG and dU.  Lane j of a half-warp divides for the half-warp's block j (4 rows x 2).
         float m[8];
@@ -206,7 +236,7 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
         {
             const float m0 = h & 1 ? m[1] : m[0], m1 = h & 1 ? m[3] : m[2], m2 = h & 1 ? m[5] : m[4], m3 = h & 1 ? m[7] : m[6];
             const float x = h & 4 ? (h & 2 ? m3 : m2) : (h & 2 ? m1 : m0);
-            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), p.status);
+            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), AGAIN ? p.status : nullptr);
             const uint32_t r = r0 + 32 * (h & 3), kb = fb + ((h >> 2) & 1) * fblocks;
             if (h < 8 && r < p.rows && in_bounds((uint64_t)kb * p.rows + r, 1, (uint64_t)2 * fblocks * p.rows, p.status))
                 p.row_scales[(size_t)kb * p.rows + r] = s.scale;
@@ -245,8 +275,9 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
             float x = 0.0f;
 #pragma unroll
             for (int w = 0; w < 16; ++w) x = amax_nan(x, s_max[(w * 3 + a) * 128 + k]);
-            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), p.status);
+            const Fp8Scale s = fp8_block_scale(__float_as_uint(x), AGAIN ? p.status : nullptr);
             s_factor[a * 128 + k] = s.factor;
+            if (!AGAIN && abs_bits(x) >= 0x7F800000u) *s_again = 1;     // the columns' maxima are over all that the rows' are
             const uint32_t col = fb * 128 + k;
             if (a < 2) {
                 const uint64_t at = (uint64_t)rb * F2 + a * p.F + col;
@@ -271,6 +302,19 @@ fp8_gated_backward_kernel(const GatedBwdParams p) {
             }
         }
     }
+}
+
+__global__ void __launch_bounds__(kGatedBwdThreads, 1)
+fp8_gated_backward_kernel(const GatedBwdParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    int* s_again = reinterpret_cast<int*>(smem + kGatedBwdSmem - 16);
+    if (threadIdx.x == 0) *s_again = 0;
+    griddep_wait();
+    griddep_launch();
+    __syncthreads();
+    gated_backward_tiles<false>(p, smem);
+    __syncthreads();
+    if (*s_again) gated_backward_tiles<true>(p, smem);
 }
 
 }  // namespace nvq

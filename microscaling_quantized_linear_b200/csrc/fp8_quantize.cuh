@@ -32,10 +32,11 @@ struct Fp8Scale {
     float scale, factor;
 };
 
-// Scale and factor of a block from the FP32 bits of its largest magnitude.
+// Scale and factor of a block from the FP32 bits of its largest magnitude; one that is not finite is reported
+// (status null: not reported).
 __device__ __forceinline__ Fp8Scale fp8_block_scale(uint32_t amax_bits, unsigned int* status) {
     const float b = __uint_as_float(amax_bits);
-    if (amax_bits >= 0x7F800000u) atomicOr(status, kStatusNonfinite);
+    if (amax_bits >= 0x7F800000u && status) atomicOr(status, kStatusNonfinite);
     if (b < kAmaxFloor) return {0.0f, 0.0f};
     return {__fdiv_rn(b, 448.0f), __fdiv_rn(448.0f, b)};
 }
