@@ -114,6 +114,12 @@ __device__ __forceinline__ float careful_mul(float a, float b, float f) {
     return __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(a, 0x1p-64f), __fmul_rn(b, 0x1p-64f)), f), 0x1p64f), 0x1p64f);
 }
 
+// v where it is finite, w elsewhere.
+__device__ __forceinline__ uint64_t or_finite(uint64_t v, uint64_t w) {
+    const float2 a = f32x2_unpack(v), b = f32x2_unpack(w);
+    return f32x2_pack(abs_bits(a.x) < 0x7F800000u ? a.x : b.x, abs_bits(a.y) < 0x7F800000u ? a.y : b.y);
+}
+
 // The larger magnitude, NaN if either is.
 __device__ __forceinline__ float amax_nan(float m, float v) {
     float o;
@@ -139,8 +145,8 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64
 // CTA has no registers left, the 96 results of a thread hold them.
 //
 // A product of two BF16 values is exact in FP32, so it comes first.  It may pass FP32's range though the result does
-// not: a CTA that met a result which is not finite goes through its tiles once more (AGAIN), carefully in the octets
-// where that is so, and the others give the same bits.  (Looking at the inputs' magnitudes first cost every tile 3 %,
+// not: a CTA that met a result which is not finite goes through its tiles once more (AGAIN), carefully for the values
+// where that is so, and the others keep their bits.  (Looking at the inputs' magnitudes first cost every tile 3 %,
 // doing such a tile again inside the loop 17 %, by its spills.)
 template <bool AGAIN>
 __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, uint8_t* smem) {
@@ -193,9 +199,9 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
                     if (decltype(careful)::value) {
                         const float2 h = f32x2_unpack(dh), u = f32x2_unpack(up), fv = f32x2_unpack(f);
                         const uint64_t silu = f32x2_mul(gate, s);                   // at most |gate|
-                        d[0][i][e] = f32x2_pack(careful_mul(h.x, u.x, fv.x), careful_mul(h.y, u.y, fv.y));
-                        d[1][i][e] = f32x2_mul(dh, silu);
-                        d[2][i][e] = f32x2_mul(up, silu);
+                        d[0][i][e] = or_finite(d[0][i][e], f32x2_pack(careful_mul(h.x, u.x, fv.x), careful_mul(h.y, u.y, fv.y)));
+                        d[1][i][e] = or_finite(d[1][i][e], f32x2_mul(dh, silu));
+                        d[2][i][e] = or_finite(d[2][i][e], f32x2_mul(up, silu));
                     } else {
                         d[0][i][e] = f32x2_mul(f32x2_mul(dh, up), f);
                         d[1][i][e] = f32x2_mul(f32x2_mul(dh, gate), s);

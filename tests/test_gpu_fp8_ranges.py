@@ -127,3 +127,19 @@ def test_gated_backward_far_values_leave_the_others_alone(far):
     assert torch.equal(cc[:, cols], cc2[:, cols]) and torch.equal(cs[:, cols], cs2[:, cols])
     assert torch.equal(cc[128:], cc2[128:]) and torch.equal(hc[128:], hc2[128:])
     assert torch.equal(hc[:, [c for c in range(256) if c != 17]], hc2[:, [c for c in range(256) if c != 17]])
+
+
+def test_gated_backward_values_beside_a_far_one_keep_their_bits():
+    """up times a gate of 20 passes FP32 for one value of many octets: its neighbours' gradients and H stay, to the bit."""
+    g = torch.Generator().manual_seed(4)
+    gu, dh = torch.randn(256, 512, generator=g).bfloat16(), torch.randn(256, 256, generator=g).bfloat16()
+    gu[:, 9:256:16] = 20.0
+    _, (cc, cs), (hc, hs) = nvq.fp8_block_gated_backward(dh.cuda(), gu.cuda())
+    gu[:, 256 + 9::16] = 2.0 ** 126
+    dh[:, 9::16] = 2.0 ** -60
+    _, (cc2, cs2), (hc2, hs2) = nvq.fp8_block_gated_backward(dh.cuda(), gu.cuda())
+    assert torch.isinf(hs2[:, 9::16]).all() and nvq.device_status() == nvq.NVQ_STATUS_NONFINITE
+    rest = [c for c in range(256) if c % 16 != 9]
+    assert torch.equal(hc[:, rest], hc2[:, rest]) and torch.equal(hs[:, rest], hs2[:, rest])
+    rest += [256 + c for c in rest]
+    assert torch.equal(cc[:, rest], cc2[:, rest]) and torch.equal(cs[:, rest], cs2[:, rest])
