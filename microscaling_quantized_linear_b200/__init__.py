@@ -550,7 +550,10 @@ def _new(like, shape, dtype, _empty=torch.empty_strided):
     return _empty(shape, (shape[1], 1), dtype=dtype, device=like.device)
 
 
-_device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# The public functions cost a short call 2 us of 9; torch built without CUDA has only those.
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _here(stream, names, first, *rest):

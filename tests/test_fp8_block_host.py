@@ -142,3 +142,23 @@ def test_reference_codes_agree_with_torch():
                         np.random.default_rng(0).standard_normal(5000).astype(np.float32) * 40))
     t = torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     np.testing.assert_array_equal(ref.e4m3_code(x), t)
+
+
+def test_package_imports_with_a_torch_built_without_cuda():
+    """torch's private CUDA functions are not there then; the package has to load and to refuse CPU tensors."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    delattr(torch._C, n)\n"
+            "import microscaling_quantized_linear_b200 as nvq\n"
+            "assert nvq.fp8_block_scale_shape('rows', 3, 200) == (2, 3)\n"
+            "try:\n"
+            "    nvq.fp8_block_quantize(torch.zeros(4, 64, dtype=torch.bfloat16))\n"
+            "except ValueError as e:\n"
+            "    assert 'CUDA tensor' in str(e)\n"
+            "    print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "refused" in out.stdout, out.stdout + out.stderr
