@@ -17,7 +17,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Same, added to the destination (FP32 tensors: one FP32 addition per element).
+// 2-D tiled tensor store that adds to the destination (FP32 tensors: one FP32 addition per element).
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
     asm volatile(
         "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
@@ -123,12 +123,6 @@ __device__ __forceinline__ void tmem_fma2(uint64_t& acc, uint32_t lo, uint32_t h
 __device__ __forceinline__ uint64_t f32x2_fma3(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t o;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o) : "l"(a), "l"(b), "l"(c));
-    return o;
-}
-
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-    uint64_t o;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
     return o;
 }
 
