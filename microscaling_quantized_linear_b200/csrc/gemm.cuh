@@ -935,7 +935,8 @@ bsgemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
             const uint32_t mb = tile % p.num_m_blocks, nb = tile / p.num_m_blocks;
             const uint32_t buf = C::ACC_BUFS == 2 ? (t_local & 1) : 0;
             const uint32_t use = C::ACC_BUFS == 2 ? (t_local >> 1) : t_local;
-            if (!mbar_wait_bounded(tfull0 + 8 * buf, use & 1, abort_flag, p.wait_ns)) {
+            // one decision per warp: the tensor-memory loads below are warp-wide
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use & 1, abort_flag, p.wait_ns))) {
                 *abort_flag = 1;
                 atomicOr(p.status, 1u);
                 break;
