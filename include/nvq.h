@@ -386,7 +386,8 @@ NVQ_API int nvfp4_linear_short_m(const void* x, int64_t M, int64_t K, int64_t ld
  * Shapes: in a layer out = in . W^T with W [N, K], N is a multiple of 8 and K of
  * 16 (a quantizer alone takes any multiple of 8 columns); row counts are any (0:
  * an empty batch); BF16 (FP32) pitches are multiples of 8 (4) elements; pointers
- * 16-byte aligned; every matrix less than 2^31 elements.  Otherwise NVQ_ERR_SHAPE /
+ * 16-byte aligned (bias: 4); a matrix of codes, gate_up and dW less than 2^31 elements,
+ * rows times pitch of any matrix less than 2^40.  Otherwise NVQ_ERR_SHAPE /
  * NVQ_ERR_ALIGN and nothing is launched.  No entry point needs a workspace; all
  * can be captured into a CUDA graph, and calls that share no output can run at
  * the same time.  These entry points have no counterpart on the pages, whose

@@ -135,8 +135,8 @@ int launch_pair(const HostDevice& d, Fp8Gemm& g, nvq_stream_t stream) {
     return launch(kern, 2 * (tiles < pairs ? tiles : pairs), C::THREADS, C::SMEM_BYTES, stream, 2, ma, mb, mo, p);
 }
 
-// The split of the contracted axis: the most CTAs that one wave of the device holds (`room`), at least
-// two blocks to a CTA, so that the weight streams through as many SMs as possible.
+// The split of the contracted axis: the largest that makes no more than `room` CTAs and leaves each at least
+// two blocks, so that the weight streams through as many SMs as possible.
 uint32_t short_log_split(uint64_t tiles, uint64_t blocks, uint64_t room) {
     uint32_t log = 3;
     while (log > 0 && (tiles << log > room || blocks < 2u << log)) --log;
@@ -170,16 +170,23 @@ int launch_short(const HostDevice& d, const Fp8Gemm& g, nvq_stream_t stream) {
     p.T = g.p.T;
     p.ldo = (uint32_t)g.ldo;
     const uint64_t tiles = (uint64_t)blocks_of(p.C) * ((p.M + TN - 1) / TN);
+    // Where two CTAs fit an SM, as many as fill half of the SMs twice: at 8 tokens (us, cold weights; columns x
+    // contracted) 1, 3/2 and 2 CTAs an SM took 14.6, 12.7 and 12.7 (12288 x 4096), 10.6, 10.6 and 14.2 (9224 x
+    // 4112), 12.9, 12.9 and 11.3 (4096 x 12288), 6.7 each (4096 x 4096).
     p.log_split = short_log_split(tiles, blocks_of(p.T), C::PER_SM == 2 ? (uint64_t)d.num_sms * 3 / 2 : d.num_sms);
     p.wait_ns = (uint32_t)host_wait_ns(kFp8WaitNs);
     return launch(kern, (uint32_t)tiles << p.log_split, C::THREADS, C::SMEM_BYTES, stream, 1u << p.log_split, mw, ma, p);
 }
 
 // Whether a product runs on the few-tokens kernel: always up to 32 tokens; above, on tiles of 64 tokens,
-// where that is estimated faster than 256-row tiles on CTA pairs.  The estimates (ns) are fits to
-// measurements: a wave of CTA pairs takes 550 a block (4096 columns, 4096 contracted, 48 to 512 tokens:
-// 20.5 to 21.5 us), a wave of few-tokens CTAs 360 a block (gated: 1000) and 3500 (9.6 us at 48 tokens,
-// 10.3 at 128, 15.3 at 256, 31 in two waves at 384).
+// where that is estimated faster than 256-row tiles on CTA pairs.  The estimates (ns) are fits: a wave of CTA
+// pairs takes 550 a block and 2500, a wave of few-tokens CTAs 360 a block (gated: 1000) and 3500.  Measured
+// (us, cold weights; columns x contracted, tokens: pairs / few-tokens):
+//   linear 4096 x 4096, 64: 21.2 / 8.4, 256: 21.6 / 16.3, 384: 21.8 / 31.2;  12288 x 4096, 64: 22.7 / 16.4, 96: 23.1 / 28.4
+//   linear 4096 x 12288, 256: 54.0 / 39.2, 384: 54.2 / 77.1;  1024 x 8192, 512: 37.4 / 16.3
+//   dgrad 4096 x 12288, 64: 52.6 / 14.4, 256: 53.1 / 39.0, 384: 53.4 / 76.8;  12288 x 4096, 64: 21.6 / 16.7, 96: 21.8 / 28.6
+//   gated 12288 x 4096, 64: 44.9 / 34.0, 96: 45.3 / 52.6;  2048 x 4096, 256: 23.7 / 19.5, 384: 23.9 / 32.0
+// Of 144 cases (16 shapes, 33 to 512 tokens) it takes the faster one in 143, in the other one 1 % slower.
 bool use_short(bool gated, int64_t R, int64_t C, int64_t T, int64_t num_sms) {
     if (R <= 32) return true;
     const int64_t blocks = blocks_of(T), tiles = blocks_of(C) * ((R + 63) / 64);

@@ -50,8 +50,8 @@ struct Fp8ShortCfg {
     static constexpr int THREADS = 352;
     static constexpr int W_BYTES = 128 * 128, A_BYTES = TN * 128;
     static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;               // of one unit (block and projection)
-    // Two CTAs to an SM: the next launch's start (barriers, tensor memory, the weight's way into L2) then
-    // overlaps this one's end.  For more tokens the exchange area leaves no room for that.
+    // Two CTAs to an SM: the next launch's start (barriers, tensor memory) then overlaps this one's end.  For
+    // more tokens the exchange area leaves no room for that.
     static constexpr int PER_SM = !GATED && TN <= 32 ? 2 : 1;
     static constexpr int TM_COLS = 512 / PER_SM;
     static constexpr int NBUF = TM_COLS / TN;                           // accumulators; unit u uses u % NBUF
