@@ -445,9 +445,11 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
             uint64_t acc[64] = {};                          // columns 2i, 2i + 1 of the unit
             for (uint32_t t = 0; t < blocks; ++t, ++it) {
                 const uint32_t b = h + 2 * (it & 1);
-                if (sslot % C::GROUP == 0 && !fp8_wait_warp(sfull0 + 8 * (sslot / C::GROUP), sphase, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
+                // A lane whose wait for scales gives up says so and goes on with what the slot holds; the warp leaves at
+                // its next wait for an accumulator that is not there yet (a vote here cost 1 to 2 % of the kernel).
+                if (sslot % C::GROUP == 0) {
+                    if (!fp8_wait(sfull0 + 8 * (sslot / C::GROUP), sphase, abort_flag, p.wait_ns)) gave_up();
+                    __syncwarp();
                 }
                 const uint32_t block_scale = scales + sslot * C::SLOT_BYTES;
                 if (++sslot == (uint32_t)C::SLOTS) {
@@ -494,9 +496,8 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 __syncwarp();
                 // the loads have returned, and the signal publishes no memory writes
                 if (lane == 0) mbar_arrive_relaxed_cluster(b == h ? release0 : release1);
-                // look at the next block's accumulator while the last chunk is added (the votes here and in the waits
-                // cost 1 to 2 % of the kernel; one in the wait itself, ready or not, 2 to 3 %; going on after a lost wait
-                // and voting once a group of scales 2 to 5 %)
+                // look at the next block's accumulator while the last chunk is added (a vote at the wait itself, ready or
+                // not, cost 2 to 3 % of the kernel; going on after any lost wait and voting once a group of scales 2 to 5 %)
                 ready = __all_sync(0xFFFFFFFFu, mbar_test(tfull0 + 8 * (b ^ 2), ((it + 1) >> 1) & 1));
                 add(7);
                 if (sslot % C::GROUP == 0) {
@@ -530,18 +531,20 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 }
                 // The row's block of 128 columns is shared by the two warps of this lane quarter.  They wait for
                 // different accumulators, so one may have given up where the other has not: it says so in place of
-                // its maximum, both come to the barrier once a tile and leave after the same one.
+                // its maximum, both come to the barrier once a tile and leave after the same one, before they make
+                // anything of what a lost wait left.
                 constexpr uint32_t kGaveUp = 0xFFFFFFFFu;  // magnitudes are below 2^31
                 uint32_t* am = s_amax + 256 * slot + 32 * q + lane;
-                am[128 * h] = ok ? m : kGaveUp;
+                if (!ok || *abort_flag) m = kGaveUp;
+                am[128 * h] = m;
                 named_barrier_sync(1 + q, 64);
                 const uint32_t other = am[128 * (h ^ 1)];
                 slot ^= 1;                                 // the next tile's writes may pass this one's reads
-                if (!ok || __any_sync(0xFFFFFFFFu, other == kGaveUp)) {
+                m = max(m, other);
+                if (__any_sync(0xFFFFFFFFu, m == kGaveUp)) {
                     ok = false;
                     break;
                 }
-                m = max(m, other);
                 if (r < p.R) {
                     const Fp8Scale s = fp8_block_scale(m, p.status);
                     const uint64_t at = (uint64_t)r * p.C + n0 + 64 * h;
