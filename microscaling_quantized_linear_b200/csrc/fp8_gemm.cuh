@@ -157,9 +157,8 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const vo
 
 // The same for a whole warp, with one decision: each lane reads the abort flag and the clock for itself, and
 // what follows a wait (tensor-memory loads, barriers, __syncwarp) takes every lane.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool fp8_wait_warp(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
-    return __all_sync(0xFFFFFFFFu, fp8_wait<CLUSTER>(bar, parity, abort, limit_ns));
+    return __all_sync(0xFFFFFFFFu, fp8_wait(bar, parity, abort, limit_ns));
 }
 
 // Warps of plain loads, each with a stage of its own: the proxy fence that publishes
