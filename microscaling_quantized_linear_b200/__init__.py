@@ -847,7 +847,8 @@ class BlockFp8Linear:
         return fp8_block_linear(codes, scales, *self.w, bias=self.bias, stream=stream), tuple(saved)
 
     def backward(self, dy, saved, dw=None, stream=None):
-        """(dx BF16, dw FP32, db FP32 or None without a bias); dw given is added to."""
+        """(dx BF16, dw FP32, db FP32 or None without a bias); dw given is added to.
+        db is torch's sum over dy's rows, one more read of dy."""
         rc, rs, cc, cs = fp8_block_quantize_both(dy, stream=stream)
         dx = fp8_block_linear_dgrad(rc, rs, *self.w, stream=stream)
         dw = fp8_block_linear_wgrad(cc, cs, *saved, out=dw, accumulate=dw is not None, stream=stream)

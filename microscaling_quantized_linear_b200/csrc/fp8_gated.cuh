@@ -38,8 +38,8 @@ struct GatedBwdParams {
 };
 
 // sigma(g) and 1 - sigma(g) of two values.  exp(-g) = 2^i 2^f with i the integer
-// nearest to -g log2(e), f the rest to about 2^-25 (log2(e) in two floats, so that a
-// large |g| costs no precision), and 2^f, |f| <= 1/2, by its Taylor series to the
+// nearest to -g log2(e), f the rest to about 2^-25 (Cody and Waite's reduction: log2(e) in two floats, so that
+// a large |g| costs no precision), and 2^f, |f| <= 1/2, by its Taylor series to the
 // seventh power (the next term is below 2^-27): 0.44 units rms against 0.67 for
 // expf and 0.97 for one ex2.approx.  The reciprocal is the approximate one and a
 // Newton step.  WIDE takes any g: it is limited to +-87, and beyond, the smaller of the two (less than
@@ -137,8 +137,8 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64
 // Persistent, one CTA per SM, over tiles of 128 rows x 128 of F; thread: rows
 // g + 32 i (i < 4) x 8 columns, its 96 results in registers.  The next tile's
 // inputs come in meanwhile (16-byte copies, each thread its own, no barrier).  11 bytes
-// a value move, which HBM does in 97 us at 4608 x 12288; measured 138 (4.6 TB/s).  The
-// arithmetic sets the pace, 53 instructions a value with packed pairs throughout: issue
+// a value move, which HBM does in 97 us at 4608 x 12288; measured 138 in short runs (4.6 TB/s), 139 to 149 over
+// seconds on different boxes.  The arithmetic sets the pace, 53 instructions a value with packed pairs throughout: issue
 // slots are 60 % full, and multiply-adds (41 % of their unit), maxima (49 %) and
 // conversions take turns, as the two barriers of a tile keep the 16 warps in step.
 // Three-operand maxima changed nothing (141.1 -> 140.9 us); a second

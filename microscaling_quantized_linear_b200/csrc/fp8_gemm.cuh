@@ -41,18 +41,19 @@
 // through a first-level cache that shared memory has left almost nothing of, and
 // cost up to a third of the kernel's time, hence the register split.
 //
-// Measured at 4608 x 12288 x 4096, values from normal ones: 230 us in short runs (2,017
-// TFLOP/s, SM clock 1.7 GHz), 276 us over seconds (1,680 TFLOP/s, at the power limit;
-// a BF16 library product reaches 1,360 there); dgrad 4608 x 4096 x 12288 224 us,
-// wgrad 357 us (its column scales are one more multiply and a shared-memory read for
-// each pair of values), gated 512 us short and 590 us with gate and up kept.
+// Measured at 4608 x 12288 x 4096, values from normal ones, on several boxes: 230 to 236 us in
+// short runs (1,970 to 2,017 TFLOP/s, SM clock 1.7 GHz), 276 to 284 us over seconds (1,630 to
+// 1,680 TFLOP/s, at the power limit; a BF16 library product reaches 1,360 there); in short runs dgrad
+// 4608 x 4096 x 12288 224 to 232 us, wgrad 355 us (its column scales are one more multiply and a
+// shared-memory read for each pair of values), gated with gate and up kept 524 us (590 to 610 over seconds).
 // What bounds it is the epilogue: about 1,010 cycles a block, of which 500 drain and
 // add, 200 the scales, 100 to 200 each the accumulator's barrier and the release, and
 // 200 a tile's share of output; shared memory answers slowly beside the tensor core's
 // operand reads.  Tried and not kept: 16 epilogue warps of 64 columns (1,240 cycles), 32-byte
 // stores from registers in place of the staged tensor-map stores (1,230), the next block's
 // scales read before the last chunk is added (244 us against 230), longer chunks (spills).
-// Every wait is bounded (status word and abort flag), as in gemm_pair.cuh.
+// Every wait is bounded (status word and abort flag), as in gemm_pair.cuh; warps that share a barrier, and
+// the lanes of a warp, leave together when one runs out.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

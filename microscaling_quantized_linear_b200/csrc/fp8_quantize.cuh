@@ -15,8 +15,8 @@
 // within the half-warp on packed pairs of BF16 magnitudes; column maxima go
 // through 2 KB of shared memory.  The divisions are shared out, one block per
 // lane, and the factors handed round.  Bound by HBM: 2 bytes read and 1 (or 2)
-// written per value; 4608 x 12288 both ways takes 38.4 us (6.0 TB/s, 92 % of the copy
-// rate), a weight of 9224 x 4112 18.8 us (6.05 TB/s, 93 %).  One token is all launch:
+// written per value; 4608 x 12288 both ways takes 38.4 to 40.6 us on different boxes (87 to 92 % of the copy
+// rate), a weight of 9224 x 4112 18.8 to 19.6 us (89 to 93 %).  One token is all launch:
 // 10 us a call, of which the kernel's own time is hidden behind the next call's checks.
 #pragma once
 #include <cstdint>

@@ -13,9 +13,10 @@
 // tensor memory (512 / TN of them in turn); 8 epilogue warps, a thread per weight
 // row, scale it into registers.  The CTAs of a cluster then hand their partial
 // sums to each token's owner through distributed shared memory, which adds them
-// in rank order.  Measured: 29 x 9224 x 4112 11.8 us, 3.3 TB/s (stream 5.8, first tile
-// 1.1, exchange and output 2.5, start 1); gated 1 x 12288 x 4096 19.1 us, 5.3 TB/s; 1 x 4096
-// x 4096 4.9 us back to back in a graph, 9 through the binding.
+// in rank order.  Measured back to back in a graph, with the weight in HBM (weights rotated over more than L2)
+// and in L2: 29 x 9224 x 4112 11.8 and 8.7 us (3.2 TB/s from HBM; stream 5.8, first tile 1.1, exchange and output
+// 2.5, start 1), 1 x 4096 x 4096 6.4 and 4.4 us (9 through the binding), 29 x 12288 x 4096 14.1 and 10.1, dgrad 8 x
+// 4096 x 12288 11.7 and 8.5, gated 1 x 12288 x 4096 18.7 and 17.5 us (5.4 TB/s from HBM).
 // Warps 0-7: epilogue (linear: half of the tokens each group of four; gated: gate
 // and up); 8: loads; 9, 10: MMAs, units in turn.
 #pragma once
