@@ -77,14 +77,14 @@ def test_products_return_when_their_waits_run_out(make, M, N, K):
                                         (gated, 2000, 4096, 512), (wgrad, 1111, 2056, 1552)], ids=lambda v: v.__name__ if callable(v) else str(v))
 def test_a_product_that_gives_up_returns_soon(make, M, N, K):
     """No CTA of a pair drains its loads for seconds after the other gave up: 10 ms for each of at most six
-    stages, and a tenth of a second for all else."""
+    stages is far from the 4 s that one of them would take."""
     call = make(M, N, K)
     want = call()
     torch.cuda.synchronize()
     for limit_ns in (1, 500, 1000, 2000, 4000):
         start = time.monotonic()
         limited(call, limit_ns)
-        assert time.monotonic() - start < 6 * 0.01 + 0.1
+        assert time.monotonic() - start < 1.0
     assert same_bits(call(), want) and nvq.device_status() == 0
 
 
