@@ -145,7 +145,7 @@ __device__ __forceinline__ uint2 fp8_codes8(const uint64_t (&v)[4], const uint64
 // CTA has no registers left, the 96 results of a thread hold them.
 //
 // A product of two BF16 values is exact in FP32, so it comes first.  It may pass FP32's range though the result does
-// not: a CTA that met a result which is not finite goes through its tiles once more (AGAIN), carefully for the values
+// not: a CTA does its tiles that met a result which is not finite once more at the end (AGAIN), carefully for the values
 // where that is so, and the others keep their bits.  (Looking at the inputs' magnitudes first cost every tile 3 %,
 // doing such a tile again inside the loop 17 %, by its spills.)
 template <bool AGAIN>
@@ -153,7 +153,7 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
     uint4* in = reinterpret_cast<uint4*>(smem);                     // [2][12][512]
     float* s_max = reinterpret_cast<float*>(smem + 2 * 12 * 512 * 16);          // [16 warps][3][128]
     float* s_factor = s_max + 16 * 3 * 128;                                     // [3][128]
-    int* s_again = reinterpret_cast<int*>(s_factor + 3 * 128);
+    uint32_t* s_again = reinterpret_cast<uint32_t*>(s_factor + 3 * 128);        // bit n % 128: the CTA's tile n is to be done again
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t h = lane & 15, g = tid >> 4;
     const uint32_t fblocks = p.F / 128, mblocks = (p.rows + 127) / 128, tiles = fblocks * mblocks;
@@ -174,12 +174,18 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
         }
     };
     uint32_t b = 0;
-    if (blockIdx.x < tiles) load(blockIdx.x, 0);
+    if (!AGAIN && blockIdx.x < tiles) load(blockIdx.x, 0);
     cp_async_commit();
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, b ^= 1) {
-        if (tile + gridDim.x < tiles) load(tile + gridDim.x, b ^ 1);
+        if (AGAIN) {
+            const uint32_t n = tile / gridDim.x;
+            if (!(s_again[(n >> 5) & 3] >> (n & 31) & 1)) continue;
+            load(tile, b);
+        } else if (tile + gridDim.x < tiles) {
+            load(tile + gridDim.x, b ^ 1);
+        }
         cp_async_commit();
-        cp_async_wait<1>();
+        cp_async_wait<AGAIN ? 0 : 1>();
         const uint32_t fb = tile % fblocks, rb = tile / fblocks;
         const uint32_t c = fb * 128 + h * 8, r0 = rb * 128 + g;
         uint64_t d[3][4][4];                            // dG, dU, H: pairs of columns
@@ -283,7 +289,10 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
             for (int w = 0; w < 16; ++w) x = amax_nan(x, s_max[(w * 3 + a) * 128 + k]);
             const Fp8Scale s = fp8_block_scale(__float_as_uint(x), AGAIN ? p.status : nullptr);
             s_factor[a * 128 + k] = s.factor;
-            if (!AGAIN && abs_bits(x) >= 0x7F800000u) *s_again = 1;     // the columns' maxima are over all that the rows' are
+            if (!AGAIN && abs_bits(x) >= 0x7F800000u) {                 // the columns' maxima are over all that the rows' are
+                const uint32_t n = tile / gridDim.x;
+                atomicOr(s_again + ((n >> 5) & 3), 1u << (n & 31));
+            }
             const uint32_t col = fb * 128 + k;
             if (a < 2) {
                 const uint64_t at = (uint64_t)rb * F2 + a * p.F + col;
@@ -313,14 +322,15 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
 __global__ void __launch_bounds__(kGatedBwdThreads, 1)
 fp8_gated_backward_kernel(const GatedBwdParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    int* s_again = reinterpret_cast<int*>(smem + kGatedBwdSmem - 16);
-    if (threadIdx.x == 0) *s_again = 0;
+    uint4* s_again = reinterpret_cast<uint4*>(smem + kGatedBwdSmem - 16);
+    if (threadIdx.x == 0) *s_again = make_uint4(0, 0, 0, 0);
     griddep_wait();
     griddep_launch();
     __syncthreads();
     gated_backward_tiles<false>(p, smem);
     __syncthreads();
-    if (*s_again) gated_backward_tiles<true>(p, smem);
+    const uint4 again = *s_again;
+    if (again.x | again.y | again.z | again.w) gated_backward_tiles<true>(p, smem);
 }
 
 }  // namespace nvq

@@ -143,3 +143,32 @@ def test_gated_backward_values_beside_a_far_one_keep_their_bits():
     assert torch.equal(hc[:, rest], hc2[:, rest]) and torch.equal(hs[:, rest], hs2[:, rest])
     rest += [256 + c for c in rest]
     assert torch.equal(cc[:, rest], cc2[:, rest]) and torch.equal(cs[:, rest], cs2[:, rest])
+
+
+def test_gated_backward_far_values_of_many_tiles_per_block():
+    """20,480 tiles, some 139 to a thread block: far values early, late and in a block's first, its 128th and its last
+    tiles are done carefully, and a NaN stays where it is."""
+    M, F = 2, 128 * 20480
+    g = torch.Generator("cuda").manual_seed(5)
+    gu, dh = (torch.randn(M, n, generator=g, device="cuda").bfloat16() for n in (2 * F, F))
+    clean = nvq.fp8_block_gated_backward(dh, gu)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = [0, 7, sms - 1, sms, 127 * sms + 5, 128 * sms, 130 * sms + 9, 20479]
+    cols = torch.tensor([128 * t + 3 for t in tiles], device="cuda")
+    gu[:, cols], gu[:, F + cols], dh[:, cols] = -40.0, 2.0 ** 126, 1.0
+    gu[1, F + 128 * 50 + 9] = float("nan")
+    (rc, rs), (cc, cs), (hc, hs) = nvq.fp8_block_gated_backward(dh, gu)
+    assert nvq.device_status() == nvq.NVQ_STATUS_NONFINITE
+    want = abs(ref.silu(np.float64(-40.0)) * 2.0 ** 126)
+    inside(hs[0, cols].double().cpu().numpy(), np.float64(want / 448), (want * sigmoid_error(np.float64(40.0)) + 2.0 ** -23 * want) / 448)
+    bad = ~torch.isfinite(hs)
+    assert bad[0, 128 * 50 + 9] and bad.sum() == 1
+    bad = ~torch.isfinite(cs)
+    assert bad[0, 128 * 50 + 9] and bad.sum() == 1
+    bad = ~torch.isfinite(rs)
+    assert bad[50, 1] and bad.sum() == 1
+    same = torch.ones(F, dtype=torch.bool, device="cuda")
+    same[cols], same[128 * 50 + 9] = False, False
+    assert torch.equal(hs[:, same], clean[2][1][:, same]) and torch.equal(hc[:, same], clean[2][0][:, same])
+    same = torch.cat((same, same))
+    assert torch.equal(cs[:, same], clean[1][1][:, same]) and torch.equal(cc[:, same], clean[1][0][:, same])
