@@ -199,9 +199,15 @@ __device__ __forceinline__ void gated_backward_tiles(const GatedBwdParams& p, ui
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint64_t dh = pair(wh[e]), gate = pair(wg[e]), up = pair(wu[e]);
-                    uint64_t s, om;
+                    uint64_t s, om, k;                               // k = 1 + gate (1 - s)
                     sigmoid2<decltype(wide)::value>(gate, s, om);
-                    const uint64_t f = f32x2_mul(s, f32x2_fma3(gate, om, f32x2_pack(1.0f, 1.0f)));
+                    const uint64_t one = f32x2_pack(1.0f, 1.0f);
+                    // Around gate = -1.28, where k is 0, s is small beside 1 - s: (1 + gate) - gate s, with 1 + gate exact there,
+                    // takes k's error from that of 1 - s = e s to that of s (dG 13.1 -> 5.6 units of 2^-24 rms, the FP32
+                    // formula in separate operations 7.1, gates of standard deviation 1.5; 1 % slower)
+                    if (decltype(wide)::value) k = f32x2_fma3(gate, om, one);
+                    else k = f32x2_fma3(pair(wg[e] ^ 0x80008000u), s, f32x2_add(gate, one));
+                    const uint64_t f = f32x2_mul(s, k);
                     if (decltype(careful)::value) {
                         const float2 h = f32x2_unpack(dh), u = f32x2_unpack(up), fv = f32x2_unpack(f);
                         const uint64_t silu = f32x2_mul(gate, s);                   // at most |gate|

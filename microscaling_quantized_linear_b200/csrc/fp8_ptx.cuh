@@ -126,6 +126,12 @@ __device__ __forceinline__ uint64_t f32x2_fma3(uint64_t a, uint64_t b, uint64_t 
     return o;
 }
 
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+    uint64_t o;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
+    return o;
+}
+
 __device__ __forceinline__ uint64_t f32x2_mul(uint64_t p, uint64_t s) {
     uint64_t o;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(p), "l"(s));

@@ -172,3 +172,16 @@ def test_gated_backward_far_values_of_many_tiles_per_block():
     assert torch.equal(hs[:, same], clean[2][1][:, same]) and torch.equal(hc[:, same], clean[2][0][:, same])
     same = torch.cat((same, same))
     assert torch.equal(cs[:, same], clean[1][1][:, same]) and torch.equal(cc[:, same], clean[1][0][:, same])
+
+
+def test_gated_backward_where_the_derivative_of_silu_vanishes():
+    """dgate around gate = -1.28, dH = up = 1: its error is the sigmoid's, not magnified by a rounded 1 - sigmoid.
+    sigma is within 1.5 FP32 steps (2^-23), so that 1 + g - g sigma is off by |g| sigma 1.5 2^-23; three more roundings.
+    One row: the column scales are |dgate| / 448 to FP32 precision."""
+    g = torch.arange(0xBF80, 0xBFD0, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16)      # -1.0 to -1.6171875
+    gu = torch.cat((torch.cat((g, g[:128 - len(g)]))[None], torch.ones(1, 128, dtype=torch.bfloat16)), 1)
+    _, (_, cs), _ = nvq.fp8_block_gated_backward(torch.ones(1, 128, dtype=torch.bfloat16, device="cuda"), gu.cuda())
+    G = gu[0, :128].double().numpy()
+    s = 1 / (1 + np.exp(-G))
+    f = s * (1 + G * (1 - s))
+    inside(cs[0, :128].double().cpu().numpy() * 448, np.abs(f), s * np.abs(G) * s * 1.5 * 2.0 ** -23 + 4 * 2.0 ** -24 * np.abs(f))
